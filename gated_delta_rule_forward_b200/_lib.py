@@ -17,6 +17,8 @@ EXPORTS = (
     "gdr_forward_launches", "gdr_forward_kernel_name", "gdr_status_string",
     "gdr_last_error", "gdr_version", "gdr_device_status", "gdr_forward_chunked_noalloc",
     "gdr_forward_plan", "gdr_forward_segment_parts", "gdr_backward_workspace_size", "gdr_backward",
+    "gdr_linear_workspace_size", "gdr_linear_forward", "gdr_linear_backward", "gdr_linear_decode_step",
+    "gdr_copy_states",
 )
 
 STATUS = {0: "GDR_OK", 1: "GDR_ERR_INVALID_ARG", 2: "GDR_ERR_UNSUPPORTED", 3: "GDR_ERR_ALIGNMENT",
@@ -33,6 +35,21 @@ class BwdGrads(ctypes.Structure):
     """Mirror of gdr_bwd_grads_t (include/gdr.h)."""
     _fields_ = [(name, ctypes.c_void_p) for name in ("dq", "dk", "dv", "dbeta", "dlog_g", "d_initial_state",
                                                       "d_erase_b", "d_write_w")]
+
+
+class LinearArgs(ctypes.Structure):
+    """Mirror of gdr_linear_args_t (include/gdr.h)."""
+    _fields_ = ([(name, ctypes.c_void_p) for name in ("q", "k", "v")]
+                + [(name, ctypes.c_longlong * 3) for name in ("q_stride", "k_stride", "v_stride")]
+                + [(name, ctypes.c_void_p) for name in ("log_decay", "cu_seqlens", "state_slots")]
+                + [("pages", ctypes.c_int)]
+                + [(name, ctypes.c_void_p) for name in ("initial_state", "final_state", "o")])
+
+
+class LinearGrads(ctypes.Structure):
+    """Mirror of gdr_linear_grads_t (include/gdr.h)."""
+    _fields_ = [("d_o", ctypes.c_void_p), ("d_o_stride", ctypes.c_longlong * 3)] + [
+        (name, ctypes.c_void_p) for name in ("d_final_state", "dq", "dk", "dv", "d_initial_state")]
 
 
 _lock = threading.Lock()
@@ -78,6 +95,17 @@ def lib() -> ctypes.CDLL:
             L.gdr_backward.argtypes = ([i] * 7 + [ctypes.POINTER(FwdArgs), vp, vp, ctypes.POINTER(BwdGrads), f, f,
                                                  vp, sz, vp])
             L.gdr_backward.restype = i
+            L.gdr_linear_workspace_size.argtypes = [i] * 10
+            L.gdr_linear_workspace_size.restype = sz
+            L.gdr_linear_forward.argtypes = [i] * 8 + [ctypes.POINTER(LinearArgs), f, vp, sz, vp]
+            L.gdr_linear_forward.restype = i
+            L.gdr_linear_backward.argtypes = ([i] * 8 + [ctypes.POINTER(LinearArgs), ctypes.POINTER(LinearGrads), f,
+                                                         vp, sz, vp])
+            L.gdr_linear_backward.restype = i
+            L.gdr_linear_decode_step.argtypes = [i] * 6 + [vp] * 5 + [i] + [vp] * 2 + [f, vp]
+            L.gdr_linear_decode_step.restype = i
+            L.gdr_copy_states.argtypes = [vp] + [i] * 5 + [ctypes.POINTER(i)] * 2 + [i, vp]
+            L.gdr_copy_states.restype = i
             _lib = L
         return _lib
 

@@ -10,6 +10,8 @@
 #include "gdr.h"
 #include "chunk_bwd.cuh"
 #include "chunk_split.cuh"
+#include "linear.cuh"
+#include "state_copy.cuh"
 
 namespace {
 
@@ -390,6 +392,286 @@ gdr_status_t gdr_decode_step(int variant, int dtype, int N, int H, int dk, int d
   p.beta = beta; p.log_g = log_g; p.erase_b = erase_b; p.write_w = write_w;
   p.state = state; p.o = o; p.eps = eps; p.scale = scale;
   return check_cuda(gdr_launch_decode(p, static_cast<cudaStream_t>(stream)), "decode launch");
+}
+
+// ------------------------------------------------------------------ linear attention with a decay per head
+
+static int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 148;   // no device: the B200's, for size queries
+  }
+  return sms;
+}
+
+// The shape checks of the forward, the backward and the workspace query.
+static gdr_status_t validate_linear(int dtype, int B, int T, int Hk, int H, int dk, int dv, int N, bool packed) {
+  if (dtype != GDR_F32 && dtype != GDR_BF16) return fail(GDR_ERR_INVALID_ARG, "dtype must be GDR_F32 or GDR_BF16");
+  if (!valid_dim(dk) || !valid_dim(dv)) return fail(GDR_ERR_UNSUPPORTED, "dk and dv must each be 64 or 128");
+  if (B < 0 || T < 0 || Hk < 0 || H < 0 || N < 0) return fail(GDR_ERR_INVALID_ARG, "B, T, Hk, H and N must be >= 0");
+  if (H > 0 && (Hk == 0 || H % Hk != 0)) return fail(GDR_ERR_INVALID_ARG, "H must be a multiple of Hk");
+  if (H > 16384) return fail(GDR_ERR_UNSUPPORTED, "at most 16384 heads");
+  if (packed && B != 1) return fail(GDR_ERR_INVALID_ARG, "packed sequences need B = 1");
+  if (!packed && N != B) return fail(GDR_ERR_INVALID_ARG, "N must be B without cu_seqlens");
+  if (static_cast<long long>(T) + N > (1ll << 30) || static_cast<long long>(B) * T > (1ll << 40))
+    return fail(GDR_ERR_UNSUPPORTED, "too many tokens");
+  return GDR_OK;
+}
+
+// Fills `t` from a pointer and its (batch, token, head) strides; all zero strides mean a dense tensor.
+static gdr_status_t linear_tensor(gdr::LinTensor *t, const void *p, const long long st[3], int B, int T, int heads,
+                                  int d, int div, int esize, const char *name) {
+  if (!p) return fail(GDR_ERR_INVALID_ARG, std::string(name) + " is required");
+  if (!aligned16(p)) return fail(GDR_ERR_ALIGNMENT, std::string(name) + " must be 16-byte aligned");
+  const long long dense[3] = {static_cast<long long>(T) * heads * d, static_cast<long long>(heads) * d, d};
+  const int extent[3] = {B, T, heads};
+  long long use[3];
+  const bool given = st[0] || st[1] || st[2];
+  for (int i = 0; i < 3; ++i) {
+    use[i] = given && extent[i] > 1 ? st[i] : dense[i];   // the stride of a single entry is never followed
+    if (extent[i] > 1 && (use[i] < d || use[i] * esize % 16 != 0 || use[i] >= (1ll << 38)))
+      return fail(GDR_ERR_INVALID_ARG, std::string(name) +
+                  ": batch, token and head strides must be at least d, multiples of 16 bytes and below 2^38 elements");
+  }
+  *t = {p, use[0], use[1], use[2], div};
+  return GDR_OK;
+}
+
+static gdr::LinRun linear_run(int ia, int ib, int ic, int da, int dc, int reverse, float bscale, float yscale, void *y) {
+  gdr::LinRun r = {};
+  r.ia = ia; r.ib = ib; r.ic = ic; r.da = da; r.dc = dc;
+  r.reverse = reverse; r.bscale = bscale; r.yscale = yscale; r.y = y;
+  return r;
+}
+
+// The shape of a call (runs without tensors or states), planned for the current device.
+static void linear_shape(gdr::LinProblem *p, int dtype, int B, int T, int H, int dk, int dv, int N, bool packed,
+                         bool backward) {
+  *p = {};
+  for (gdr::LinTensor &t : p->t) t.div = 1;
+  p->bf16_io = dtype == GDR_BF16;
+  p->B = B; p->T = T; p->H = H; p->N = N;
+  static const int some_cu = 0;
+  p->cu = packed ? &some_cu : nullptr;   // replaced by the caller's; the plan only asks whether there is one
+  if (backward) {
+    p->nrun = 3;
+    p->run[0] = linear_run(3, 2, 1, dv, dk, 0, 1.f, 1.f, nullptr);   // dq = run(dO, v, k)
+    p->run[1] = linear_run(1, 0, 3, dk, dv, 1, 1.f, 1.f, nullptr);   // dv = reverse run(k, q, dO)
+    p->run[2] = linear_run(2, 3, 0, dv, dk, 1, 1.f, 1.f, nullptr);   // dk = reverse run(v, dO, q)
+  } else {
+    p->nrun = 1;
+    p->run[0] = linear_run(0, 1, 2, dk, dv, 0, 1.f, 1.f, nullptr);   // o = run(q, k, v)
+  }
+  gdr_linear_plan(p, sm_count());
+}
+
+static size_t linear_state_bytes(const gdr::LinProblem &p) { return (gdr_linear_workspace_bytes(p) + 255) / 256 * 256; }
+
+size_t gdr_linear_workspace_size(int dtype, int B, int T, int Hk, int H, int dk, int dv, int N, int packed,
+                                 int backward) {
+  if (validate_linear(dtype, B, T, Hk, H, dk, dv, N, packed != 0) != GDR_OK) return 0;
+  if (T == 0 || H == 0 || N == 0) return 0;
+  gdr::LinProblem p;
+  linear_shape(&p, dtype, B, T, H, dk, dv, N, packed != 0, backward != 0);
+  size_t bytes = linear_state_bytes(p);
+  // shared key heads: dq and dk of every value head, in fp32, before they are summed
+  if (backward && H != Hk) bytes += 2 * sizeof(float) * static_cast<size_t>(B) * T * H * dk;
+  return bytes;
+}
+
+static gdr_status_t linear_states(const gdr_linear_args_t *a) {
+  if ((a->initial_state && !aligned16(a->initial_state)) || (a->final_state && !aligned16(a->final_state)))
+    return fail(GDR_ERR_ALIGNMENT, "state pointers must be 16-byte aligned");
+  return GDR_OK;
+}
+
+gdr_status_t gdr_linear_forward(int dtype, int B, int T, int Hk, int H, int dk, int dv, int N,
+                                const gdr_linear_args_t *a, float scale, void *workspace, size_t workspace_bytes,
+                                void *stream) {
+  if (!a) return fail(GDR_ERR_INVALID_ARG, "args is NULL");
+  gdr_status_t st = validate_linear(dtype, B, T, Hk, H, dk, dv, N, a->cu_seqlens != nullptr);
+  if (st != GDR_OK) return st;
+  if (N == 0 || H == 0) return GDR_OK;
+  if (a->state_slots && a->pages < 0) return fail(GDR_ERR_INVALID_ARG, "pages must be >= 0");
+  if ((st = linear_states(a)) != GDR_OK) return st;
+  if (!a->log_decay) return fail(GDR_ERR_INVALID_ARG, "log_decay is required");
+  gdr::LinProblem p;
+  linear_shape(&p, dtype, B, T, H, dk, dv, N, a->cu_seqlens != nullptr, false);
+  const int es = dtype == GDR_BF16 ? 2 : 4;
+  if (T > 0) {
+    if ((st = linear_tensor(&p.t[0], a->q, a->q_stride, B, T, Hk, dk, H / Hk, es, "q")) != GDR_OK) return st;
+    if ((st = linear_tensor(&p.t[1], a->k, a->k_stride, B, T, Hk, dk, H / Hk, es, "k")) != GDR_OK) return st;
+    if ((st = linear_tensor(&p.t[2], a->v, a->v_stride, B, T, H, dv, 1, es, "v")) != GDR_OK) return st;
+    if (!a->o) return fail(GDR_ERR_INVALID_ARG, "o is required");
+    if (!aligned16(a->o)) return fail(GDR_ERR_ALIGNMENT, "o must be 16-byte aligned");
+  }
+  const size_t need = T > 0 ? gdr_linear_workspace_bytes(p) : 0;
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(GDR_ERR_INVALID_ARG, "the workspace must be at least gdr_linear_workspace_size() bytes");
+  if (need && !aligned16(workspace)) return fail(GDR_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  if (T == 0 && !a->final_state) return GDR_OK;
+  if (injected_launch_fault()) return fail(GDR_ERR_CUDA, "injected launch failure (GDR_FAULT=launch)");
+  p.cu = a->cu_seqlens; p.slots = a->state_slots; p.pages = a->state_slots ? a->pages : N;
+  p.log_decay = a->log_decay;
+  gdr::LinRun &r = p.run[0];
+  r.yscale = scale; r.y = a->o; r.s0 = a->initial_state; r.s_final = a->final_state;
+  std::string err;
+  const cudaError_t e = gdr_launch_linear(p, workspace, static_cast<cudaStream_t>(stream), &err);
+  if (e != cudaSuccess) return fail(GDR_ERR_CUDA, "linear forward: " + err + cudaGetErrorString(e));
+  return GDR_OK;
+}
+
+gdr_status_t gdr_linear_backward(int dtype, int B, int T, int Hk, int H, int dk, int dv, int N,
+                                 const gdr_linear_args_t *a, const gdr_linear_grads_t *g, float scale,
+                                 void *workspace, size_t workspace_bytes, void *stream) {
+  if (!a || !g) return fail(GDR_ERR_INVALID_ARG, "args and grads are required");
+  gdr_status_t st = validate_linear(dtype, B, T, Hk, H, dk, dv, N, a->cu_seqlens != nullptr);
+  if (st != GDR_OK) return st;
+  if (a->state_slots) return fail(GDR_ERR_UNSUPPORTED, "the backward takes no state slots");
+  if (N == 0 || H == 0) return GDR_OK;
+  if ((st = linear_states(a)) != GDR_OK) return st;
+  if ((g->d_final_state && !aligned16(g->d_final_state)) || (g->d_initial_state && !aligned16(g->d_initial_state)))
+    return fail(GDR_ERR_ALIGNMENT, "state pointers must be 16-byte aligned");
+  if (!a->log_decay) return fail(GDR_ERR_INVALID_ARG, "log_decay is required");
+  gdr::LinProblem p;
+  linear_shape(&p, dtype, B, T, H, dk, dv, N, a->cu_seqlens != nullptr, true);
+  const int es = dtype == GDR_BF16 ? 2 : 4;
+  if (T > 0) {
+    if ((st = linear_tensor(&p.t[0], a->q, a->q_stride, B, T, Hk, dk, H / Hk, es, "q")) != GDR_OK) return st;
+    if ((st = linear_tensor(&p.t[1], a->k, a->k_stride, B, T, Hk, dk, H / Hk, es, "k")) != GDR_OK) return st;
+    if ((st = linear_tensor(&p.t[2], a->v, a->v_stride, B, T, H, dv, 1, es, "v")) != GDR_OK) return st;
+    if ((st = linear_tensor(&p.t[3], g->d_o, g->d_o_stride, B, T, H, dv, 1, es, "d_o")) != GDR_OK) return st;
+    if (!g->dq || !g->dk || !g->dv) return fail(GDR_ERR_INVALID_ARG, "dq, dk and dv are required");
+    if (!aligned16(g->dq) || !aligned16(g->dk) || !aligned16(g->dv))
+      return fail(GDR_ERR_ALIGNMENT, "dq, dk and dv must be 16-byte aligned");
+  }
+  const size_t need = gdr_linear_workspace_size(dtype, B, T, Hk, H, dk, dv, N, a->cu_seqlens != nullptr, 1);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(GDR_ERR_INVALID_ARG, "the workspace must be at least gdr_linear_workspace_size() bytes");
+  if (need && !aligned16(workspace)) return fail(GDR_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  if (T == 0 && !g->d_initial_state) return GDR_OK;
+  if (injected_launch_fault()) return fail(GDR_ERR_CUDA, "injected launch failure (GDR_FAULT=launch)");
+  p.cu = a->cu_seqlens; p.pages = N;
+  p.log_decay = a->log_decay;
+  float *dq32 = nullptr, *dk32 = nullptr;
+  if (H != Hk && T > 0) {
+    dq32 = reinterpret_cast<float *>(static_cast<char *>(workspace) + linear_state_bytes(p));
+    dk32 = dq32 + static_cast<size_t>(B) * T * H * dk;
+  }
+  gdr::LinRun &rq = p.run[0], &rv = p.run[1], &rk = p.run[2];
+  rq.yscale = scale; rq.s0 = a->initial_state; rq.s0_t = 1;
+  rv.bscale = scale; rv.s0 = g->d_final_state; rv.s_final = g->d_initial_state;
+  rk.bscale = scale; rk.s0 = g->d_final_state; rk.s0_t = 1;
+  rq.y = dq32 ? dq32 : g->dq; rq.y_f32 = dq32 != nullptr;
+  rk.y = dk32 ? dk32 : g->dk; rk.y_f32 = dk32 != nullptr;
+  rv.y = g->dv;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  std::string err;
+  cudaError_t e = gdr_launch_linear(p, workspace, s, &err);
+  if (e == cudaSuccess && dq32) {
+    err = "group sum: ";
+    e = gdr_launch_linear_group_sum(dq32, g->dq, dtype == GDR_BF16, B, T, Hk, H / Hk, dk, a->cu_seqlens, N, s);
+    if (e == cudaSuccess)
+      e = gdr_launch_linear_group_sum(dk32, g->dk, dtype == GDR_BF16, B, T, Hk, H / Hk, dk, a->cu_seqlens, N, s);
+  }
+  if (e != cudaSuccess) return fail(GDR_ERR_CUDA, "linear backward: " + err + cudaGetErrorString(e));
+  return GDR_OK;
+}
+
+gdr_status_t gdr_linear_decode_step(int dtype, int N, int Hk, int H, int dk, int dv, const void *q, const void *k,
+                                    const void *v, const float *log_decay, float *state, int pages,
+                                    const int *state_slots, void *o, float scale, void *stream) {
+  if (dtype != GDR_F32 && dtype != GDR_BF16) return fail(GDR_ERR_INVALID_ARG, "dtype must be GDR_F32 or GDR_BF16");
+  if (!valid_dim(dk) || !valid_dim(dv)) return fail(GDR_ERR_UNSUPPORTED, "dk and dv must each be 64 or 128");
+  if (N < 0 || Hk < 0 || H < 0 || pages < 0) return fail(GDR_ERR_INVALID_ARG, "N, Hk, H and pages must be >= 0");
+  if (H > 0 && (Hk == 0 || H % Hk != 0)) return fail(GDR_ERR_INVALID_ARG, "H must be a multiple of Hk");
+  if (static_cast<long long>(N) * H * (dv / 32) >= (1ll << 31)) return fail(GDR_ERR_UNSUPPORTED, "N * H is too large");
+  if (static_cast<long long>(N) * H == 0) return GDR_OK;
+  if (!state_slots && pages < N) return fail(GDR_ERR_INVALID_ARG, "without state_slots the pool needs N pages");
+  if (!q || !k || !v || !o || !log_decay || (!state && pages > 0))
+    return fail(GDR_ERR_INVALID_ARG, "q, k, v, o, log_decay and state are required");
+  const void *io[5] = {q, k, v, o, state};
+  for (const void *p : io)
+    if (!aligned16(p)) return fail(GDR_ERR_ALIGNMENT, "q, k, v, o and state must be 16-byte aligned");
+  if (injected_launch_fault()) return fail(GDR_ERR_CUDA, "injected launch failure (GDR_FAULT=launch)");
+  gdr::LinDecodeProblem p;
+  p.N = N; p.Hk = Hk; p.H = H; p.dk = dk; p.dv = dv; p.pages = pages;
+  p.bf16_io = dtype == GDR_BF16;
+  p.q = q; p.k = k; p.v = v; p.log_decay = log_decay; p.slots = state_slots; p.state = state; p.o = o;
+  p.scale = scale;
+  return check_cuda(gdr_launch_linear_decode(p, sm_count(), static_cast<cudaStream_t>(stream)), "linear decode launch");
+}
+
+// ------------------------------------------------------------------ state pages
+
+namespace {
+
+// Marks of the pages in the launch being gathered: a fixed open-addressing
+// table on the stack, at most two entries per pair.
+struct PageMarks {
+  static constexpr int kSize = 2048;   // > 2 * kMaxCopyPairs, a power of two
+  int key[kSize];
+  unsigned char mark[kSize];
+  void clear() { std::memset(mark, 0, sizeof(mark)); }
+  unsigned char &at(int page) {
+    unsigned i = (static_cast<unsigned>(page) * 2654435761u) >> 21;   // 11 bits
+    while (mark[i] && key[i] != page) i = (i + 1) & (kSize - 1);
+    key[i] = page;
+    return mark[i];
+  }
+};
+
+}  // namespace
+
+gdr_status_t gdr_copy_states(float *pool, int layers, int pages, int H, int dk, int dv, const int *src, const int *dst,
+                             int n, void *stream) {
+  if (layers < 0 || pages < 0 || H < 0 || n < 0) return fail(GDR_ERR_INVALID_ARG, "layers, pages, H and n must be >= 0");
+  if (!valid_dim(dk) || !valid_dim(dv)) return fail(GDR_ERR_UNSUPPORTED, "dk and dv must each be 64 or 128");
+  if (n > 0 && (!src || !dst)) return fail(GDR_ERR_INVALID_ARG, "src and dst are required");
+  for (int i = 0; i < n; ++i) {
+    if (src[i] < -1 || src[i] >= pages)
+      return fail(GDR_ERR_INVALID_ARG, "src[" + std::to_string(i) + "] = " + std::to_string(src[i]) + " is no page of " +
+                                           std::to_string(pages) + " (and not -1, which clears)");
+    if (dst[i] < 0 || dst[i] >= pages)
+      return fail(GDR_ERR_INVALID_ARG, "dst[" + std::to_string(i) + "] = " + std::to_string(dst[i]) + " is no page of " +
+                                           std::to_string(pages));
+  }
+  if (n == 0 || layers == 0 || H == 0) return GDR_OK;
+  if (!pool) return fail(GDR_ERR_INVALID_ARG, "pool is required");
+  if (!aligned16(pool)) return fail(GDR_ERR_ALIGNMENT, "pool must be 16-byte aligned");
+  const size_t page_floats = static_cast<size_t>(H) * dk * dv;
+  const size_t per_page = (page_floats + 8191) / 8192;
+  if (per_page > (1u << 20) || per_page * layers * gdr::kMaxCopyPairs >= (1ull << 31))
+    return fail(GDR_ERR_UNSUPPORTED, "the pages are too large");
+  if (injected_launch_fault()) return fail(GDR_ERR_CUDA, "injected launch failure (GDR_FAULT=launch)");
+  // The pairs act one after another.  Pairs go into one launch while none reads or
+  // writes a page that an earlier one of it writes, or writes one that it reads.
+  constexpr unsigned char kRead = 1, kWritten = 2;
+  gdr::CopyPairs batch;
+  PageMarks marks;
+  batch.n = 0;
+  marks.clear();
+  for (int i = 0; i <= n; ++i) {
+    if (i < n && src[i] == dst[i]) continue;
+    const bool clash = i < n && batch.n > 0 &&
+                       (marks.at(dst[i]) || (src[i] >= 0 && (marks.at(src[i]) & kWritten)));
+    if (batch.n > 0 && (i == n || clash || batch.n == gdr::kMaxCopyPairs)) {
+      const gdr_status_t st = check_cuda(
+          gdr_launch_state_copy(pool, page_floats, layers, pages, batch, static_cast<cudaStream_t>(stream)), "state copy launch");
+      if (st != GDR_OK) return st;
+      batch.n = 0;
+      marks.clear();
+    }
+    if (i == n) break;
+    batch.src[batch.n] = src[i];
+    batch.dst[batch.n] = dst[i];
+    ++batch.n;
+    marks.at(dst[i]) |= kWritten;
+    if (src[i] >= 0) marks.at(src[i]) |= kRead;
+  }
+  return GDR_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,168 @@
+// Linear attention with a decay per head: the problem description shared by
+// its kernels, and the device helpers that read it.
+//
+// With lambda = exp(log_decay[h]) the operator is
+//     S_t = lambda S_{t-1} + k_t v_t^T,     o_t = scale S_t^T q_t,
+// and its gradients are three more runs of the same recurrence:
+//     dq_t = scale S_t dO_t                        = run(a = dO, b = v,  c = k)
+//     dv_s = dS_s^T k_s                            = reverse run(a = k,  b = q,  c = dO)
+//     dk_s = dS_s v_s                              = reverse run(a = v,  b = dO, c = q)
+//     dS_t = scale q_t dO_t^T + lambda dS_{t+1}    (the reverse runs' state, or its transpose)
+// so every kernel here computes a "run" of three tensors a, b, c:
+//     forward:  S <- lambda S + bscale b c^T,  y = yscale S^T a
+//     reverse:  S <- S + bscale b c^T,         y = yscale S^T a,   S <- lambda S
+// with S [da][dc].  The reverse state is carried with the decay to the next
+// (earlier) token applied, so that what a run leaves is the gradient of the
+// initial state, and its start is the gradient of the final state.
+//
+// Long sequences are cut into segments of `seg` tokens that run side by side:
+// phase 1 leaves every segment's end state from a zero start, a chain kernel
+// turns those into start states, and phase 2 runs all segments from them.
+#pragma once
+
+#include <string>
+
+#include "common.cuh"
+
+namespace gdr {
+
+constexpr int kLinMaxRuns = 3;
+
+// A [B, T, heads, d] tensor with unit stride along d; value head h reads head h / div.
+struct LinTensor {
+  const void *p;
+  long long sb, st, sh;   // elements
+  int div;
+};
+
+struct LinRun {
+  int ia, ib, ic;       // indexes into LinProblem::t
+  int da, dc;
+  int reverse;
+  float bscale, yscale;
+  void *y;              // [B, T, H, dc], dense
+  int y_f32;            // y in fp32 instead of the I/O type
+  const float *s0;      // start state [.., H, da, dc], or null (zeros)
+  int s0_t;             // s0 is laid out [.., H, dc, da]
+  float *s_final;       // end state [.., H, da, dc], or null
+  float *X;             // [items, H, da, dc] segment states, used when segmented
+};
+
+struct LinProblem {
+  int nrun;
+  LinRun run[kLinMaxRuns];
+  LinTensor t[4];
+  bool bf16_io;
+  int B, T, H, N;        // N sequences: N = B, or the packed ones of B = 1
+  const int *cu;         // [N + 1] token offsets of the packed sequences, or null
+  const int *slots;      // [N] page of each sequence's state, or null (page n)
+  int pages;
+  const float *log_decay;   // [H]
+  int seg;               // tokens per segment (a multiple of 64)
+  int G;                 // dense: segments per sequence
+  int items;             // (sequence, segment) pairs, an upper bound when packed
+};
+
+#ifdef __CUDACC__
+// One (sequence, segment).  `ok` is false for an index past the last segment.
+struct LinItem {
+  bool ok;
+  int n, g, nseg, b;
+  int t0, len;   // the sequence's first token within its batch row, its length
+};
+
+__device__ __forceinline__ int lin_cu(const LinProblem &p, int n) { return min(max(__ldg(p.cu + n), 0), p.T); }
+
+// Sequence n's items start at cu[n] / seg + n: consecutive starts differ by at
+// least the sequence's segments (and by at least one for an empty sequence), so
+// a packed batch needs no table.  The search is 32-ary, one probe per lane;
+// offsets are clamped to [0, T], so that any cu_seqlens stays within the rows.
+__device__ __forceinline__ LinItem lin_item(const LinProblem &p, int x) {
+  LinItem it;
+  if (!p.cu) {
+    it.n = x / p.G;
+    it.g = x - it.n * p.G;
+    it.b = it.n;
+    it.t0 = 0;
+    it.len = p.T;
+    it.nseg = p.G;
+    it.ok = true;
+    return it;
+  }
+  const int lane = threadIdx.x & 31;
+  int lo = 0, cnt = p.N;
+  bool found = true;
+  while (true) {
+    const int step = (cnt + 31) / 32;
+    const int i = lane * step;
+    const bool le = i < cnt && lin_cu(p, lo + i) / p.seg + lo + i <= x;
+    const unsigned m = __ballot_sync(0xffffffffu, le);
+    if (m == 0) {
+      found = false;
+      break;
+    }
+    const int k = 31 - __clz(m);
+    lo += k * step;
+    cnt = min(step, cnt - k * step);
+    if (step == 1) break;
+  }
+  it.n = lo;
+  it.b = 0;
+  it.t0 = lin_cu(p, lo);
+  it.len = max(lin_cu(p, lo + 1) - it.t0, 0);
+  it.nseg = max(1, (it.len + p.seg - 1) / p.seg);
+  it.g = x - (it.t0 / p.seg + lo);
+  it.ok = found && it.g < it.nseg;
+  return it;
+}
+
+// Page of sequence n's state, or -1 where its slot lies outside the pool.
+__device__ __forceinline__ int lin_page(const LinProblem &p, int n) {
+  if (!p.slots) return n;
+  const int s = __ldg(p.slots + n);
+  return s >= 0 && s < p.pages ? s : -1;
+}
+
+// exp(n * log_decay), the product's rounding error carried into the result;
+// lambda^0 = 1 for every decay, -inf included.
+__device__ __forceinline__ float lin_pow(float log_decay, int n) {
+  if (n == 0) return 1.f;
+  const float x = log_decay * static_cast<float>(n);
+  if (!(x > -200.f)) return x <= -200.f ? 0.f : x;   // zero in fp32; NaN stays
+  const float e = fmaf(log_decay, static_cast<float>(n), -x);
+  return expf(x) * (1.f + e);
+}
+#endif
+
+}  // namespace gdr
+
+// Launchers.  `phase1`: end states of all segments but each sequence's last
+// (in the run's order) from zero, into X; otherwise the whole runs, segments
+// starting from X where a sequence has more than one.
+cudaError_t gdr_launch_linear_token(const gdr::LinProblem &p, bool phase1, bool pdl, cudaStream_t s);
+cudaError_t gdr_launch_linear_chain(const gdr::LinProblem &p, bool pdl, cudaStream_t s);
+
+// A whole call: the plan (segment length) is gdr_linear_plan's, `ws` holds
+// gdr_linear_workspace_bytes.
+void gdr_linear_plan(gdr::LinProblem *p, int sms);
+size_t gdr_linear_workspace_bytes(const gdr::LinProblem &p);
+cudaError_t gdr_launch_linear(gdr::LinProblem &p, void *ws, cudaStream_t s, std::string *err);
+
+// y[b,t,hk,:] = sum over the group's heads of x[b,t,hk * G + i,:], for the tokens of the packed
+// sequences (all tokens when cu is null).
+cudaError_t gdr_launch_linear_group_sum(const float *x, void *y, bool bf16, int B, int T, int Hk, int G, int d,
+                                        const int *cu, int N, cudaStream_t s);
+
+namespace gdr {
+struct LinDecodeProblem {
+  int N, Hk, H, dk, dv, pages;
+  bool bf16_io;
+  const void *q, *k, *v;      // [N, Hk, dk], [N, Hk, dk], [N, H, dv], dense
+  const float *log_decay;     // [H]
+  const int *slots;           // [N] or null
+  float *state;               // [pages, H, dk, dv]
+  void *o;                    // [N, H, dv]
+  float scale;
+};
+}  // namespace gdr
+cudaError_t gdr_launch_linear_decode(const gdr::LinDecodeProblem &p, int sms, cudaStream_t s);

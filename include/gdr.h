@@ -285,6 +285,120 @@ gdr_status_t gdr_backward(int variant, int dtype, int B, int T, int H, int dk, i
                           void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Linear attention with a decay per head: the recurrence without the erase
+ * term,
+ *     S_t = lambda S_{t-1} + k_t v_t^T,     o_t = S_t^T (scale * q_t),
+ * with lambda = exp(log_decay[h]) one constant per value head (the plain
+ * additive linear attention that "Kaczmarz Linear Attention" and "What Matters
+ * in Linearizing Language Models?" set the delta rule against, with a fixed
+ * forgetting rate).  log_decay <= 0; -inf keeps only the current token, 0
+ * forgets nothing.  Differences from the delta-rule entry points:
+ *  - key heads may be shared: q, k have Hk heads, v and o have H, H a multiple
+ *    of Hk, and value head h reads key head h / (H / Hk);
+ *  - q, k and v (and the backward's d_o) may be strided: unit stride along d,
+ *    and batch, token and head strides that are multiples of 16 bytes; three
+ *    zero strides mean a dense tensor.  Outputs and states are dense;
+ *  - a packed batch: cu_seqlens (device, int32, N + 1 non-decreasing offsets
+ *    from 0 to at most T) cuts the T tokens of one row (B = 1) into N
+ *    sequences, which may be empty; rows behind the last sequence are not
+ *    written.  Offsets outside [0, T] are taken as 0 or T.  Without
+ *    cu_seqlens N = B;
+ *  - state_slots (device, int32, N) makes initial_state and final_state pools
+ *    of `pages` states, sequence n's in page state_slots[n].  A slot outside
+ *    [0, pages) reads zeros and writes nothing.  The slots inside the pool must
+ *    differ from one another.
+ * A NaN or an infinity in q, k or v reaches, besides the tokens after its own,
+ * at most the other tokens of its block of 64 (bf16; the fp32 kernels keep the
+ * token order).
+ */
+typedef struct {
+    const void *q;               /* [B,T,Hk,dk] I/O dtype */
+    const void *k;               /* [B,T,Hk,dk] I/O dtype */
+    const void *v;               /* [B,T,H,dv] I/O dtype */
+    long long q_stride[3];       /* batch, token and head strides, in elements; all 0: dense */
+    long long k_stride[3];
+    long long v_stride[3];
+    const float *log_decay;      /* [H] */
+    const int *cu_seqlens;       /* [N+1] or NULL */
+    const int *state_slots;      /* [N] or NULL (state n) */
+    int pages;                   /* pages of the state pools; used with state_slots */
+    const float *initial_state;  /* [N,H,dk,dv] or [pages,H,dk,dv], or NULL for zeros */
+    float *final_state;          /* as initial_state, or NULL; may be the same buffer */
+    void *o;                     /* [B,T,H,dv] I/O dtype (forward only) */
+} gdr_linear_args_t;
+
+typedef struct {
+    const void *d_o;             /* [B,T,H,dv] I/O dtype */
+    long long d_o_stride[3];     /* as q_stride */
+    const float *d_final_state;  /* [N,H,dk,dv] or NULL (zero) */
+    void *dq;                    /* [B,T,Hk,dk] I/O dtype */
+    void *dk;                    /* [B,T,Hk,dk] I/O dtype */
+    void *dv;                    /* [B,T,H,dv] I/O dtype */
+    float *d_initial_state;      /* [N,H,dk,dv], or NULL when not wanted; overlaps no other buffer */
+} gdr_linear_grads_t;
+
+/*
+ * Bytes of device workspace gdr_linear_forward (backward = 0) or
+ * gdr_linear_backward (backward = 1) needs on the current device: the states
+ * between the segments that a long sequence is cut into, and, for the backward
+ * of shared key heads, every value head's dq and dk in fp32.  `packed` says
+ * whether the call has cu_seqlens.  0 for a call without need or outside the
+ * supported shapes.
+ */
+size_t gdr_linear_workspace_size(int dtype, int B, int T, int Hk, int H, int dk, int dv, int N, int packed,
+                                 int backward);
+
+/*
+ * Whole-sequence forward.  Shapes: B, T, Hk, H, N >= 0; dk, dv in {64, 128};
+ * bf16 or fp32.  bf16 products run on the tensor cores with fp32 accumulation;
+ * the state is carried in fp32 and its update keeps fp32 accuracy; fp32 inputs
+ * are computed in fp32.  An empty sequence copies its initial state to its
+ * final state.  The workspace (16-byte aligned, overwritten) may be NULL where
+ * gdr_linear_workspace_size() is 0.
+ */
+gdr_status_t gdr_linear_forward(int dtype, int B, int T, int Hk, int H, int dk, int dv, int N,
+                                const gdr_linear_args_t *args, float scale, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of <d_o, o> + <d_final_state, S_T> with respect to q, k, v and the
+ * initial state, for the forward that `args` describes (its o and final_state
+ * are not used, and state_slots must be NULL):
+ *     dS_t = scale q_t d_o_t^T + lambda dS_{t+1}   (from d_final_state at the end)
+ *     dq_t = scale S_t d_o_t,  dk_t = dS_t v_t,  dv_t = dS_t^T k_t,  dS_init = lambda dS_0
+ * dq and dk are summed over the value heads that share a key head, in fp32 and
+ * in a fixed order.  The decays are constants of the layer and have no
+ * gradient.
+ */
+gdr_status_t gdr_linear_backward(int dtype, int B, int T, int Hk, int H, int dk, int dv, int N,
+                                 const gdr_linear_args_t *args, const gdr_linear_grads_t *grads, float scale,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token for N sequences: q, k [N,Hk,dk]; v, o [N,H,dv] (dense, I/O dtype);
+ * state [pages,H,dk,dv] fp32, updated in place in page state_slots[n] (device,
+ * int32), or in page n when state_slots is NULL.  A row whose slot lies outside
+ * [0, pages) is padding: its o is zeros and it touches no state.  The slots
+ * inside the pool must differ from one another.  One kernel launch, no
+ * workspace.
+ */
+gdr_status_t gdr_linear_decode_step(int dtype, int N, int Hk, int H, int dk, int dv, const void *q, const void *k,
+                                    const void *v, const float *log_decay, float *state, int pages,
+                                    const int *state_slots, void *o, float scale, void *stream);
+
+/*
+ * Page copies of a pool of recurrent states [layers,pages,H,dk,dv] (fp32, of
+ * any variant): for i = 0 .. n-1, one after another, page dst[i] of every layer
+ * becomes a copy of page src[i], or zeros where src[i] is -1.  Copying, forking
+ * (one source, several destinations), compacting and clearing are lists of such
+ * pairs.  src and dst are HOST arrays, checked and read before the call returns
+ * (a captured graph keeps their values).  Pairs that do not depend on one
+ * another share a launch, up to 480 of them.
+ */
+gdr_status_t gdr_copy_states(float *pool, int layers, int pages, int H, int dk, int dv, const int *src,
+                             const int *dst, int n, void *stream);
+
+/*
  * Kernel launches one gdr_forward_chunked call with these arguments makes
  * (0 if the call would be rejected), and a short name of the kernel that runs
  * ("chunk64_split", "token_f32io", "token_bf16io", or "none").
