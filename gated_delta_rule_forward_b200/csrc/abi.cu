@@ -10,7 +10,7 @@
 #include "gdr.h"
 #include "chunk_bwd.cuh"
 #include "chunk_split.cuh"
-#include "linear.cuh"
+#include "linear_chunk.cuh"
 #include "state_copy.cuh"
 
 namespace {
@@ -126,8 +126,9 @@ const char *gdr_last_error(void) { return g_last_error.c_str(); }
 gdr_status_t gdr_device_status(void *stream) {
   const int ef = gdr_read_device_error(static_cast<cudaStream_t>(stream));
   const int eb = gdr_bwd_read_device_error(static_cast<cudaStream_t>(stream));
-  if (ef < 0 || eb < 0) return fail(GDR_ERR_CUDA, "synchronisation or symbol read failed");
-  const int e = ef | eb;
+  const int el = gdr_linear_read_device_error(static_cast<cudaStream_t>(stream));
+  if (ef < 0 || eb < 0 || el < 0) return fail(GDR_ERR_CUDA, "synchronisation or symbol read failed");
+  const int e = ef | eb | el;
   if (e & 1) return fail(GDR_ERR_TIMEOUT, "a bounded device-side wait gave up");
   if (e & 2) return fail(GDR_ERR_RANGE, "a chunked-kernel operand left its representable range");
   return GDR_OK;
@@ -415,7 +416,9 @@ static gdr_status_t validate_linear(int dtype, int B, int T, int Hk, int H, int 
   if (H > 16384) return fail(GDR_ERR_UNSUPPORTED, "at most 16384 heads");
   if (packed && B != 1) return fail(GDR_ERR_INVALID_ARG, "packed sequences need B = 1");
   if (!packed && N != B) return fail(GDR_ERR_INVALID_ARG, "N must be B without cu_seqlens");
-  if (static_cast<long long>(T) + N > (1ll << 30) || static_cast<long long>(B) * T > (1ll << 40))
+  // grids hold one block per (run, segment, head, column group), segments at least 64 tokens
+  if (static_cast<long long>(T) + N > (1ll << 30) || static_cast<long long>(B) * T > (1ll << 31) / (H > 0 ? H : 1) ||
+      (static_cast<long long>(B) * T / 64 + N) * (H > 0 ? H : 1) > (1ll << 28))
     return fail(GDR_ERR_UNSUPPORTED, "too many tokens");
   return GDR_OK;
 }

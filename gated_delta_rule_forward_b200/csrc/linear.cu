@@ -1,7 +1,9 @@
 // Linear attention with a decay per head: the plan of a call, the chain of its
 // segments' start states, the sum over shared heads' gradients, and the order
-// of the launches.  The runs themselves are in linear_token.cu.
+// of the launches.  The runs themselves are in linear_chunk.cu (bf16) and
+// linear_token.cu (fp32).
 #include "linear.cuh"
+#include "linear_chunk.cuh"
 #include "tc_util.cuh"
 
 namespace gdr {
@@ -126,15 +128,28 @@ cudaError_t gdr_launch_linear_group_sum(const float *x, void *y, bool bf16, int 
 }
 
 void gdr_linear_plan(gdr::LinProblem *p, int sms) {
-  // Token kernel: one warp per (run, segment, head, 8 columns), 12 or so resident
-  // per SM; segments of at least 64 tokens until the device is full.
-  long warps = 0;
-  for (int i = 0; i < p->nrun; ++i) warps += static_cast<long>(p->H) * (p->run[i].dc / 8);
-  const long slots = 12L * sms;
   const long total = static_cast<long>(p->B) * p->T;
-  long want = (total * warps + slots - 1) / slots;        // tokens per segment that fill the slots
-  if (!p->cu && static_cast<long>(p->N) * warps >= slots) want = p->T;
-  long seg = (want + 63) / 64 * 64;
+  long seg;
+  if (p->bf16_io) {
+    // Two CTAs per SM, one per (run, segment, head).
+    const long slots = 2L * sms, heads = static_cast<long>(p->H) * p->nrun;
+    if (!p->cu) {
+      const long per_seq = slots / (heads * p->N > 0 ? heads * p->N : 1);   // segments per sequence that fit
+      seg = per_seq <= 1 ? p->T : (p->T + per_seq - 1) / per_seq;
+    } else {
+      seg = total * heads / slots;
+    }
+    if (seg < 128) seg = 128;
+  } else {
+    // Token kernel: one warp per (run, segment, head, 8 columns), 12 or so resident
+    // per SM; segments of at least 64 tokens until the device is full.
+    long warps = 0;
+    for (int i = 0; i < p->nrun; ++i) warps += static_cast<long>(p->H) * (p->run[i].dc / 8);
+    const long slots = 12L * sms;
+    seg = (total * warps + slots - 1) / slots;        // tokens per segment that fill the slots
+    if (!p->cu && static_cast<long>(p->N) * warps >= slots) seg = p->T;
+  }
+  seg = (seg + 63) / 64 * 64;
   if (seg < 64) seg = 64;
   const long whole = (p->T + 63) / 64 * 64;
   if (seg > whole) seg = whole > 0 ? whole : 64;
@@ -157,12 +172,18 @@ cudaError_t gdr_launch_linear(gdr::LinProblem &p, void *ws, cudaStream_t s, std:
     p.run[i].X = X;
     X += static_cast<size_t>(p.items) * p.H * p.run[i].da * p.run[i].dc;
   }
-  cudaError_t e;
   const bool segmented = p.T > p.seg;
+  const bool chunk = p.bf16_io && p.T > 0;   // no tokens: the token kernel copies the states
+  gdr::LinChunkMaps maps;
+  if (chunk && !gdr_linear_chunk_maps(p, &maps)) return *err = "tensor map: ", cudaErrorInvalidValue;
+  auto phase = [&](bool phase1, bool pdl) {
+    return chunk ? gdr_launch_linear_chunk(p, maps, phase1, pdl, s) : gdr_launch_linear_token(p, phase1, pdl, s);
+  };
+  cudaError_t e;
   if (segmented) {
-    if ((e = gdr_launch_linear_token(p, true, false, s)) != cudaSuccess) return *err = "segment states: ", e;
+    if ((e = phase(true, false)) != cudaSuccess) return *err = "segment states: ", e;
     if ((e = gdr_launch_linear_chain(p, true, s)) != cudaSuccess) return *err = "segment chain: ", e;
   }
-  if ((e = gdr_launch_linear_token(p, false, segmented, s)) != cudaSuccess) return *err = "token kernel: ", e;
+  if ((e = phase(false, segmented)) != cudaSuccess) return *err = "runs: ", e;
   return cudaSuccess;
 }
