@@ -9,10 +9,11 @@
 // One CTA sweeps the chunks of one (run, segment, head) in order; everything is
 // held transposed, so that M = 128 of the MMAs is the value width and the state
 // is their tensor-memory operand:
-//     P    [t][s]   = a b^T                    M64  N64  K = da   (tensor memory)
-//     O^T  [dc][t]  = S^T a^T                  M128 N64  K = da   (S^T in bf16 in tensor memory)
-//     O^T           = Gamma_t O^T + c^T P^T    M128 N64  K = 64   (P back through shared memory in bf16)
-//     dS^T [dc][da] = c^T (w b)                M128 N = da, K = 64
+//     P    [t][s]   = a b^T          M64  N64  K = da   (tensor memory)
+//     O1^T [dc][t]  = S^T a^T        M128 N64  K = da   (S^T in bf16 in tensor memory)
+//     O2^T [dc][t]  = c^T P^T        M128 N64  K = 64   (P back through shared memory in bf16)
+//     dS^T [dc][da] = c^T (w b)      M128 N = da, K = 64
+// The last three go to the tensor pipe in one go, and Y^T = yscale (Gamma_t O1^T + O2^T).
 // The fp32 state lives in registers: lane dc of a warp quad, half of da per
 // thread; S <- lambda^n S + dS is one pass over it.
 //
@@ -43,16 +44,19 @@ constexpr uint32_t TILE = 16384;        // 64 rows of two 128-byte atoms
 constexpr uint32_t OFF_A = 0;           // a (phase 1: the second c buffer)
 constexpr uint32_t OFF_C = TILE;
 constexpr uint32_t OFF_B = 2 * TILE;    // two buffers; the first term of w b replaces b in place
-constexpr uint32_t OFF_M = 4 * TILE;    // second and third terms of w b
+constexpr uint32_t OFF_M = 4 * TILE;    // second and third terms of w b; then each warp's 2 KB of output rows
 constexpr uint32_t OFF_L = 5 * TILE;
 constexpr uint32_t OFF_P = 6 * TILE;    // bf16 P, rows t, 8 KB
 constexpr uint32_t OFF_PW = OFF_P + 8192;      // lambda^0 .. lambda^64, then what fp32 loses of them
-constexpr uint32_t OFF_BAR = OFF_PW + 2 * 65 * 4 + 8;
+constexpr uint32_t OFF_D = OFF_PW + 2 * 65 * 4 + 8;   // bscale lambda^d at 64 + d, zeros for d < 0
+constexpr uint32_t OFF_BAR = OFF_D + 128 * 4;
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 128 + 1024;
 static_assert(OFF_BAR % 16 == 0 && 2 * (SMEM_BYTES + 1024) <= 233472, "two CTAs per SM");
 constexpr uint32_t COL_DS = 0;     // dS^T, 128 columns
+constexpr uint32_t COL_P = 0;      // P, 64 columns: read before dS^T is formed, formed after dS^T is read
 constexpr uint32_t COL_S = 128;    // S^T in bf16, 64 columns
-constexpr uint32_t COL_PO = 192;   // P, then O^T, 64 columns
+constexpr uint32_t COL_O2 = 128;   // O2^T over S^T: formed after O1^T, read before the next S^T
+constexpr uint32_t COL_O1 = 192;   // O1^T, 64 columns
 constexpr uint32_t TMEM_COLS = 256;
 
 // Bounded wait that also gives up once another thread has.
@@ -106,10 +110,11 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   }
 
   float *pw = reinterpret_cast<float *>(sm + OFF_PW), *pw_lo = pw + 65;
+  float *dtab = reinterpret_cast<float *>(sm + OFF_D);
   uint64_t *bar_a = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
   uint64_t *bar_b = bar_a + 1;    // [2]
   uint64_t *bar_c = bar_a + 3;    // [2], the second one in phase 1 only
-  uint64_t *bar_p = bar_a + 5, *bar_qs = bar_a + 6, *bar_kv = bar_a + 7, *bar_pv = bar_a + 8;
+  uint64_t *bar_p = bar_a + 5, *bar_o1 = bar_a + 6, *bar_o = bar_a + 7, *bar_kv = bar_a + 8;
   uint64_t *bar_drain = bar_a + 9;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_a + 10);
   volatile int *abort = reinterpret_cast<volatile int *>(bar_a + 11);
@@ -129,6 +134,10 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     const float hi = static_cast<float>(e);
     pw[m] = hi;
     pw_lo[m] = static_cast<float>(e - hi);
+    if (m < C) {
+      dtab[C + m] = r.bscale * hi;
+      dtab[m] = 0.f;
+    }
   }
   // value widths of 64: the upper 64 lanes of the M = 128 products read zeros
   if (DC == 64)
@@ -227,7 +236,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
 #pragma unroll
       for (int kk = 0; kk < DA / 16; ++kk) {
         const uint32_t o = (kk >> 2) * 8192 + (kk & 3) * 32;
-        mma_ss(tmem + COL_PO, sdesc(a + o, 16, 1024), sdesc(b + o, 16, 1024), idesc_bf16(C, C, false, false), kk > 0);
+        mma_ss(tmem + COL_P, sdesc(a + o, 16, 1024), sdesc(b + o, 16, 1024), idesc_bf16(C, C, false, false), kk > 0);
       }
       mma_commit(bar_p);
     };
@@ -257,19 +266,27 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       ok = ok && wait_or_abort(bar_p, ph, abort);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      float v[32];
-      tmem_ld32(lrow + COL_PO + 32 * half, v);
-      const int t = 16 * quad + lane;
-      if (lane < 16) {
+      float v[16];
+      tmem_ld_frag4(lrow + COL_P + 32 * half, v);
+      tmem_wait_ld();
+      uint32_t u[4][2];   // column groups of 8 x rows lane / 4 (+ 8)
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int s = 32 * half + e;
-          const bool keep = rev ? s >= t && s < n : s <= t;
-          v[e] = keep ? v[e] * (pw[keep ? (rev ? s - t : t - s) : 0] * r.bscale) : 0.f;
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int t = 16 * quad + (lane >> 2) + 8 * k, s = 32 * half + 8 * j + 2 * (lane & 3);
+          float y[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int d = rev ? s + e - t : t - s - e;
+            const float w = dtab[C + d];
+            y[e] = d >= 0 && s + e < n ? v[4 * j + 2 * k + e] * w : 0.f;
+          }
+          u[j][k] = pack_bf16x2(y[0], y[1]);
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) st_chunk_bf16(sm + OFF_P + sw128(t, 4 * half + j), v + 8 * j);
-      }
+      const int t = 16 * quad + (lane & 15), ch = 4 * half + (lane >> 4);
+      stmatrix4(smem_u32(sm + OFF_P + sw128(t, ch)), u[0][0], u[0][1], u[1][0], u[1][1]);
+      stmatrix4(smem_u32(sm + OFF_P + sw128(t, ch + 2)), u[2][0], u[2][1], u[3][0], u[3][1]);
     }
     // 2. w b in three bf16 terms; rows behind the sequence's end become zeros, in c too
     ok = ok && wait_or_abort(bar_b + (i & 1), (i >> 1) & 1, abort);
@@ -304,17 +321,17 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     tc_fence_before();
     if ((bad = __syncthreads_or(!ok))) break;
 
-    // 3. O^T = S^T a^T and dS^T = c^T (w b)
-    const uint32_t ct = smem_u32(sm + ct_off);
+    // 3. O1^T = S^T a^T, O2^T = c^T P^T and dS^T = c^T (w b)
     if (tid == 0) {
       tc_fence_after();
+      const uint32_t ct = smem_u32(sm + ct_off);
       if (!PHASE1) {
         const uint32_t a = smem_u32(sm + OFF_A);
 #pragma unroll
         for (int kk = 0; kk < DA / 16; ++kk)
-          mma_ts(tmem + COL_PO, tmem + COL_S + 8 * kk, sdesc(a + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024),
+          mma_ts(tmem + COL_O1, tmem + COL_S + 8 * kk, sdesc(a + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024),
                  idesc_bf16(128, C, false, false), kk > 0);
-        mma_commit(bar_qs);
+        mma_commit(bar_o1);
       }
       ok = wait_or_abort(bar_c + cbuf, cph, abort);
       if (ok) {
@@ -327,49 +344,28 @@ __global__ void __launch_bounds__(NTHREADS, 2)
                    idesc_bf16(128, DA, true, true), t + kk > 0);
         mma_commit(bar_kv);
       }
-    }
-    __syncwarp();
-
-    // 4. the state's part of the output takes its decays, then the tokens' part is added
-    if (!PHASE1) {
-      ok = ok && wait_or_abort(bar_qs, ph, abort);
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-      float v[32];
-      tmem_ld32(lrow + COL_PO + 32 * half, v);
-      uint32_t u[16];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int t = 32 * half + 16 * q + e;
-          u[e] = __float_as_uint(v[16 * q + e] * pw[rev ? max(n - 1 - t, 0) : t + 1]);
-        }
-        tmem_st16(lrow + COL_PO + 32 * half + 16 * q, u);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      if ((bad = __syncthreads_or(!ok))) break;
-      if (tid == 0) {
-        if (i + 1 < nch) load_a(i + 1);
-        tc_fence_after();
+      // O2^T goes where S^T was read from: once O1^T is complete, while dS^T is under way
+      if (!PHASE1 && ok && (ok = wait_or_abort(bar_o1, ph, abort))) {
         const uint32_t pt = smem_u32(sm + OFF_P);
 #pragma unroll
         for (int kk = 0; kk < C / 16; ++kk)
-          mma_ss(tmem + COL_PO, sdesc(ct + kk * 2048, 8192, 1024), sdesc(pt + kk * 32, 16, 1024),
-                 idesc_bf16(128, C, true, false), 1);
-        mma_commit(bar_pv);
+          mma_ss(tmem + COL_O2, sdesc(ct + kk * 2048, 8192, 1024), sdesc(pt + kk * 32, 16, 1024),
+                 idesc_bf16(128, C, true, false), kk > 0);
+        mma_commit(bar_o);
       }
-      __syncwarp();
     }
+    __syncwarp();
 
-    // 5. S <- lambda^n S + dS, and its operand for the next chunk
+    // 4. S <- lambda^n S + dS
     ok = ok && wait_or_abort(bar_kv, ph, abort);
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
-    if (tid == 0 && i + 2 < nch && ok) {
-      load_b(i + 2);
-      if (PHASE1) load_c(i + 2);
+    if (tid == 0 && ok) {
+      if (i + 2 < nch) {
+        load_b(i + 2);
+        if (PHASE1) load_c(i + 2);
+      }
+      if (!PHASE1 && i + 1 < nch) load_a(i + 1);
     }
     __syncwarp();
     {
@@ -386,39 +382,62 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       tc_fence_before();   // dS^T is read before the next chunk's product overwrites it
       continue;
     }
-    store_operand();
 
-    // 6. the output rows: lane dc, columns t = 32 half ..
-    ok = ok && wait_or_abort(bar_pv, ph, abort);
+    // 5. the output: this warp's 32 columns dc and 32 tokens t, through its 2 KB of
+    // shared memory (rows t of 64 bytes, 16-byte chunks XOR-ed with t / 2) unless in fp32
+    ok = ok && wait_or_abort(bar_o, ph, abort);
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
-    if (tid == 0 && i + 1 < nch && ok) load_c(i + 1);
+    if (tid == 0 && ok && i + 1 < nch) load_c(i + 1);
     __syncwarp();
-    {
-      float v[32];
-      tmem_ld32(lrow + COL_PO + 32 * half, v);
-#pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] *= r.yscale;
-      const size_t y0 = ((static_cast<size_t>(it.b) * p.T + it.t0 + row0) * p.H + h) * DC;
+    if (quad * 32 < DC) {
+      uint8_t *stage = sm + OFF_M + 2048 * warp;
+      const size_t y0 = ((static_cast<size_t>(it.b) * p.T + it.t0 + row0) * p.H + h) * DC + 32 * quad;
       const size_t ystep = static_cast<size_t>(p.H) * DC;
-      if (quad * 32 < DC) {
-        if (r.y_f32) {
-          float *y = static_cast<float *>(r.y) + y0 + dcr;
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (32 * half + e < n) y[(32 * half + e) * ystep] = v[e];
-        } else {
-          // neighbouring lanes trade halves of their tokens, so that each stores pairs of columns:
-          // even lanes the tokens 0 .. 15, odd lanes 16 .. 31
-          const bool odd = lane & 1;
-          __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(r.y) + y0 + (dcr & ~1);
+      for (int hh = 0; hh < 2; ++hh) {   // 16 lanes of tensor memory: dc = 32 quad + 16 hh ..
+        float v1[16], v2[16];
+        const uint32_t at = lrow + (static_cast<uint32_t>(16 * hh) << 16) + 32 * half;
+        tmem_ld_frag4(at + COL_O1, v1);
+        tmem_ld_frag4(at + COL_O2, v2);
+        tmem_wait_ld();
+        uint32_t u[4][2];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? v[e] : v[16 + e], 1);
-            const int t = 32 * half + e + (odd ? 16 : 0);
-            const uint32_t pair = odd ? pack_bf16x2(other, v[16 + e]) : pack_bf16x2(v[e], other);
-            if (t < n) *reinterpret_cast<uint32_t *>(y + t * ystep) = pair;
+        for (int j = 0; j < 4; ++j) {
+          const int t = 32 * half + 8 * j + 2 * (lane & 3);
+          const float g0 = pw[rev ? max(n - 1 - t, 0) : t + 1], g1 = pw[rev ? max(n - 2 - t, 0) : t + 2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float y0v = r.yscale * fmaf(g0, v1[4 * j + 2 * k], v2[4 * j + 2 * k]);
+            const float y1v = r.yscale * fmaf(g1, v1[4 * j + 2 * k + 1], v2[4 * j + 2 * k + 1]);
+            if (r.y_f32) {
+              float *y = static_cast<float *>(r.y) + y0 + 16 * hh + 8 * k + (lane >> 2);
+              if (t < n) y[t * ystep] = y0v;
+              if (t + 1 < n) y[(t + 1) * ystep] = y1v;
+            } else {
+              u[j][k] = pack_bf16x2(y0v, y1v);
+            }
           }
+        }
+        if (!r.y_f32) {
+          // matrix m: tokens 8 (j + m / 2) .., columns 16 hh + 8 (m & 1) ..; row q = token
+          const int t = 8 * (lane >> 4) + (lane & 7), ch = 2 * hh + ((lane >> 3) & 1);
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            const int tt = 8 * j + t;
+            stmatrix4_trans(smem_u32(stage + tt * 64 + ((ch ^ (tt >> 1)) & 3) * 16), u[j][0], u[j][1], u[j + 1][0],
+                            u[j + 1][1]);
+          }
+        }
+      }
+      if (!r.y_f32) {
+        __syncwarp();
+        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(r.y) + y0 + 8 * (lane & 3);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int tt = 8 * k + (lane >> 2), t = 32 * half + tt;
+          const uint4 row = *reinterpret_cast<const uint4 *>(stage + tt * 64 + (((lane & 3) ^ (tt >> 1)) & 3) * 16);
+          if (t < n) *reinterpret_cast<uint4 *>(y + t * ystep) = row;
         }
       }
     }
@@ -430,6 +449,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       if (ok) issue_p(i + 1);
     }
     __syncwarp();
+    if (i + 1 < nch) store_operand();
   }
 
   bad = __syncthreads_or(bad || !ok);
