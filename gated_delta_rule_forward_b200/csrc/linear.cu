@@ -131,8 +131,8 @@ void gdr_linear_plan(gdr::LinProblem *p, int sms) {
   const long total = static_cast<long>(p->B) * p->T;
   long seg;
   if (p->bf16_io) {
-    // Two CTAs per SM, one per (run, segment, head).
-    const long slots = 2L * sms, heads = static_cast<long>(p->H) * p->nrun;
+    // One CTA per SM and (run, segment, head).
+    const long slots = sms, heads = static_cast<long>(p->H) * p->nrun;
     if (!p->cu) {
       const long per_seq = slots / (heads * p->N > 0 ? heads * p->N : 1);   // segments per sequence that fit
       seg = per_seq <= 1 ? p->T : (p->T + per_seq - 1) / per_seq;

@@ -10,12 +10,12 @@
 // held transposed, so that M = 128 of the MMAs is the value width and the state
 // is their tensor-memory operand:
 //     P    [t][s]   = a b^T          M64  N64  K = da   (tensor memory)
+//     dS^T [dc][da] = c^T (w b)      M128 N = da, K = 64
 //     O1^T [dc][t]  = S^T a^T        M128 N64  K = da   (S^T in bf16 in tensor memory)
 //     O2^T [dc][t]  = c^T P^T        M128 N64  K = 64   (P back through shared memory in bf16)
-//     dS^T [dc][da] = c^T (w b)      M128 N = da, K = 64
-// The last three go to the tensor pipe in one go, and Y^T = yscale (Gamma_t O1^T + O2^T).
-// The fp32 state lives in registers: lane dc of a warp quad, half of da per
-// thread; S <- lambda^n S + dS is one pass over it.
+// and Y^T = yscale (Gamma_t O1^T + O2^T).  The fp32 state lives in registers of
+// 16 warps: lane dc of a quad, a quarter of da per thread; S <- lambda^n S + dS
+// is one pass over it.
 //
 // Rounding.  The products' inputs are exact bf16 except three: w b, P and the
 // S^T operand.  w b enters the state, which is fp32, so it is split into three
@@ -24,10 +24,13 @@
 // of what follows.  P and S^T enter only Y, on disjoint parts of its sum, and
 // are rounded once to bf16, like Y itself.
 //
-// Two CTAs share an SM (107 KB of shared memory, 256 tensor-memory columns, nine
-// warps of 112 registers each).  One warp issues the copies and the MMAs; the
-// others hand over to it through mbarriers only, so that the next chunk's P is
-// formed while this one's outputs are written.
+// One CTA has the SM.  Its warps are specialised and hand over through
+// mbarriers, so that three chunks are under way at once:
+//     copies (1 warp)    a, b, c of chunk i + 2 into the stage that chunk i leaves
+//     prep   (8 warps)   P and w b of chunk i + 1
+//     MMAs   (1 warp)    dS(i), P(i + 1), O1(i), O2(i)
+//     finish (16 warps)  S after chunk i, its bf16 operand, the output rows of chunk i
+// Only S -> operand -> O1 is a chain from chunk to chunk.
 #include "linear.cuh"
 #include "linear_chunk.cuh"
 #include "tc_util.cuh"
@@ -41,27 +44,27 @@ namespace tc {
 namespace {
 
 constexpr int C = 64;
-constexpr int UNROLL_W = 2;
-constexpr int NCOMPUTE = 8;                       // compute warps; one more issues copies and MMAs
-constexpr int NTHREADS = 32 * (NCOMPUTE + 1);
+constexpr int NFINISH = 16, NPREP = 8;   // warps 0 .. 15 and 16 .. 23, then the MMA and the copy warp
+constexpr int NTHREADS = 32 * (NFINISH + NPREP + 2);
 constexpr uint32_t TILE = 16384;        // 64 rows of two 128-byte atoms
-constexpr uint32_t OFF_A = 0;           // a (phase 1: the second c buffer)
-constexpr uint32_t OFF_C = TILE;
-constexpr uint32_t OFF_B = 2 * TILE;    // two buffers; the first term of w b replaces b in place
-constexpr uint32_t OFF_M = 4 * TILE;    // second and third terms of w b; then each warp's 2 KB of output rows
-constexpr uint32_t OFF_L = 5 * TILE;
-constexpr uint32_t OFF_P = 6 * TILE;    // bf16 P, rows t, 8 KB
-constexpr uint32_t OFF_PW = OFF_P + 8192;      // lambda^0 .. lambda^64, then what fp32 loses of them
-constexpr uint32_t OFF_D = OFF_PW + 2 * 65 * 4 + 8;   // yscale bscale lambda^d at 64 + d, zeros for d < 0
-constexpr uint32_t OFF_BAR = OFF_D + 128 * 4;
-constexpr uint32_t SMEM_BYTES = OFF_BAR + 128 + 1024;
-static_assert(OFF_BAR % 16 == 0 && 2 * (SMEM_BYTES + 1024) <= 233472, "two CTAs per SM");
+// one stage per chunk in flight
+constexpr uint32_t OFF_A = 0;
+constexpr uint32_t OFF_B = TILE;        // b; the first term of w b replaces it in place
+constexpr uint32_t OFF_C = 2 * TILE;
+constexpr uint32_t OFF_M = 3 * TILE;    // second and third terms of w b
+constexpr uint32_t OFF_L = 4 * TILE;
+constexpr uint32_t OFF_P = 5 * TILE;    // bf16 P, rows t, 8 KB
+constexpr uint32_t STAGE = OFF_P + 8192;
+constexpr uint32_t OFF_Y = 2 * STAGE;          // 1 KB of output rows per finishing warp
+constexpr uint32_t OFF_PW = OFF_Y + 1024 * NFINISH;   // lambda^0 .. lambda^64, then what fp32 loses of them
+constexpr uint32_t OFF_BAR = OFF_PW + 2 * 65 * 4 + 8;
+constexpr uint32_t SMEM_BYTES = OFF_BAR + 192 + 1024;
+static_assert(OFF_BAR % 16 == 0 && STAGE % 1024 == 0 && SMEM_BYTES <= 232448, "one CTA per SM");
 constexpr uint32_t COL_DS = 0;     // dS^T, 128 columns
-constexpr uint32_t COL_P = 0;      // P, 64 columns: read before dS^T is formed, formed after dS^T is read
 constexpr uint32_t COL_S = 128;    // S^T in bf16, 64 columns
-constexpr uint32_t COL_O2 = 128;   // O2^T over S^T: formed after O1^T, read before the next S^T
-constexpr uint32_t COL_O1 = 192;   // O1^T, 64 columns
-constexpr uint32_t TMEM_COLS = 256;
+constexpr uint32_t COL_P = 192;    // P, 64 columns
+constexpr uint32_t COL_O = 256;    // two buffers of O1^T and O2^T, 64 columns each
+constexpr uint32_t TMEM_COLS = 512;
 
 // Bounded wait that also gives up once another thread has.
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t phase, volatile int *abort) {
@@ -116,7 +119,7 @@ __device__ __forceinline__ void split_pair(uint32_t x, uint64_t w, uint64_t minu
 }
 
 template <int DA, int DC, bool PHASE1>
-__global__ void __launch_bounds__(NTHREADS, 2)
+__global__ void __launch_bounds__(NTHREADS, 1)
     linear_chunk_kernel(const __grid_constant__ LinProblem p, const __grid_constant__ LinChunkMaps maps,
                         const LinRunSel sel) {
   extern __shared__ uint8_t smem_raw[];
@@ -136,28 +139,35 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   }
 
   float *pw = reinterpret_cast<float *>(sm + OFF_PW), *pw_lo = pw + 65;
-  float *dtab = reinterpret_cast<float *>(sm + OFF_D);
-  uint64_t *bar_a = reinterpret_cast<uint64_t *>(sm + OFF_BAR);   // a landed
-  uint64_t *bar_b = bar_a + 1;       // [2] b landed
-  uint64_t *bar_c = bar_a + 3;       // [2] c landed (the second one in phase 1 only)
-  uint64_t *bar_p = bar_a + 5;       // P formed
-  uint64_t *bar_o1 = bar_a + 6;      // O1^T formed
-  uint64_t *bar_o = bar_a + 7;       // O2^T formed
-  uint64_t *bar_kv = bar_a + 8;      // dS^T formed
-  uint64_t *bar_ready = bar_a + 9;   // P, w b and S^T written (8 warps)
-  uint64_t *bar_ds = bar_a + 10;     // dS^T read (8 warps)
-  uint64_t *bar_drain = bar_a + 11;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_a + 12);
-  volatile int *abort = reinterpret_cast<volatile int *>(bar_a + 13);
+  // per stage (chunk i: barrier i & 1, phase (i >> 1) & 1)
+  uint64_t *bar_load = reinterpret_cast<uint64_t *>(sm + OFF_BAR);   // a, b and c landed
+  uint64_t *bar_ready = bar_load + 2;    // P and w b written (8 warps)
+  uint64_t *bar_kv = bar_load + 4;       // dS^T formed
+  uint64_t *bar_o = bar_load + 6;        // O1^T and O2^T formed
+  uint64_t *bar_oread = bar_load + 8;    // and read (16 warps)
+  // one each (chunk i: phase i & 1)
+  uint64_t *bar_p = bar_load + 10;       // P formed
+  uint64_t *bar_ds = bar_load + 11;      // dS^T read (16 warps)
+  uint64_t *bar_s = bar_load + 12;       // S^T of the chunk's start in tensor memory (16 warps)
+  uint64_t *bar_drain = bar_load + 13;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_load + 14);
+  volatile int *abort = reinterpret_cast<volatile int *>(bar_load + 15);
 
   if (warp == 0) {
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
   if (tid == 32) {
-    for (int i = 0; i < 9; ++i) mbar_init(bar_a + i, 1);
-    mbar_init(bar_ready, NCOMPUTE);
-    mbar_init(bar_ds, NCOMPUTE);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_load + i, 1);
+      mbar_init(bar_ready + i, NPREP);
+      mbar_init(bar_kv + i, 1);
+      mbar_init(bar_o + i, 1);
+      mbar_init(bar_oread + i, NFINISH);
+    }
+    mbar_init(bar_p, 1);
+    mbar_init(bar_ds, NFINISH);
+    mbar_init(bar_s, NFINISH);
     mbar_init(bar_drain, 1);
     *abort = 0;
     fence_mbar_init();
@@ -168,16 +178,12 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     const float hi = static_cast<float>(e);
     pw[m] = hi;
     pw_lo[m] = static_cast<float>(e - hi);
-    if (m < C) {
-      dtab[C + m] = r.bscale * r.yscale * hi;
-      dtab[m] = 0.f;
-    }
   }
   // value widths of 64: the upper 64 lanes of the M = 128 products read zeros
   if (DC == 64)
     for (int i = tid; i < 512; i += NTHREADS) {
       reinterpret_cast<uint4 *>(sm + OFF_C + 8192)[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (PHASE1) reinterpret_cast<uint4 *>(sm + OFF_A + 8192)[i] = make_uint4(0u, 0u, 0u, 0u);
+      reinterpret_cast<uint4 *>(sm + STAGE + OFF_C + 8192)[i] = make_uint4(0u, 0u, 0u, 0u);
     }
   fence_async_smem();
   tc_fence_before();
@@ -194,39 +200,44 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   // a state that leaves in fp32 takes all three terms; one that only makes bf16 outputs, two
   const bool three = PHASE1 || final_page;
   auto chunk_row = [&](int i) { return beg + C * (rev ? nch - 1 - i : i); };
-  bool ok = true;
 
-  if (warp == NCOMPUTE) {
-    // ---------------------------------------------------------------- issuer: copies and MMAs
+  if (warp == NFINISH + NPREP + 1) {
+    // ---------------------------------------------------------------- copies
     if (lane == 0) {
       const CUtensorMap *ma = &maps.m[r.ia], *mb = &maps.m[r.ib], *mc = &maps.m[r.ic];
       const int ha = h / p.t[r.ia].div, hb = h / p.t[r.ib].div, hc = h / p.t[r.ic].div;
+      constexpr uint32_t bytes = (PHASE1 ? 0 : DA * 128) + DA * 128 + DC * 128;
+      int i = 0;
+      for (; i < nch; ++i) {
+        const int st = i & 1, row = it.t0 + chunk_row(i);
+        uint8_t *dst = sm + STAGE * st;
+        if (i >= 2 && !wait_or_abort((PHASE1 ? bar_kv : bar_o) + st, ((i - 2) >> 1) & 1, abort)) break;
+        mbar_expect_tx(bar_load + st, bytes);
+        for (int d = 0; d < DA / 64; ++d) {
+          tma_load_4d(dst + OFF_B + 8192 * d, mb, bar_load + st, 64 * d, hb, row, it.b);
+          if (!PHASE1) tma_load_4d(dst + OFF_A + 8192 * d, ma, bar_load + st, 64 * d, ha, row, it.b);
+        }
+        for (int d = 0; d < DC / 64; ++d) tma_load_4d(dst + OFF_C + 8192 * d, mc, bar_load + st, 64 * d, hc, row, it.b);
+        if (i + 2 < nch) {   // and the chunk that comes into this stage next, as far as L2
+          const int ahead = it.t0 + chunk_row(i + 2);
+          for (int d = 0; d < DA / 64; ++d) {
+            tma_prefetch_4d(mb, 64 * d, hb, ahead, it.b);
+            if (!PHASE1) tma_prefetch_4d(ma, 64 * d, ha, ahead, it.b);
+          }
+          for (int d = 0; d < DC / 64; ++d) tma_prefetch_4d(mc, 64 * d, hc, ahead, it.b);
+        }
+      }
+      // nothing may land in shared memory after the CTA (each wait bounded)
+      for (int j = i > 2 ? i - 2 : 0; j < i; ++j) mbar_wait(bar_load + (j & 1), (j >> 1) & 1);
+    }
+  } else if (warp == NFINISH + NPREP) {
+    // ---------------------------------------------------------------- MMAs
+    if (lane == 0) {
       const uint32_t base = smem_u32(sm);
-      uint32_t issued_a = 0, issued_b = 0, issued_c = 0;
-      auto load_a = [&](int i) {
-        mbar_expect_tx(bar_a, DA * 128);
-        for (int d = 0; d < DA / 64; ++d)
-          tma_load_4d(sm + OFF_A + 8192 * d, ma, bar_a, 64 * d, ha, it.t0 + chunk_row(i), it.b);
-        ++issued_a;
-      };
-      auto load_b = [&](int i) {
-        uint64_t *bar = bar_b + (i & 1);
-        mbar_expect_tx(bar, DA * 128);
-        for (int d = 0; d < DA / 64; ++d)
-          tma_load_4d(sm + OFF_B + TILE * (i & 1) + 8192 * d, mb, bar, 64 * d, hb, it.t0 + chunk_row(i), it.b);
-        ++issued_b;
-      };
-      auto load_c = [&](int i) {
-        const int buf = PHASE1 ? i & 1 : 0;
-        mbar_expect_tx(bar_c + buf, DC * 128);
-        for (int d = 0; d < DC / 64; ++d)
-          tma_load_4d(sm + (buf ? OFF_A : OFF_C) + 8192 * d, mc, bar_c + buf, 64 * d, hc, it.t0 + chunk_row(i), it.b);
-        ++issued_c;
-      };
-      // P = a b^T once both landed
-      auto issue_p = [&](int i) -> bool {
-        if (!wait_or_abort(bar_a, i & 1, abort) || !wait_or_abort(bar_b + (i & 1), (i >> 1) & 1, abort)) return false;
-        const uint32_t a = base + OFF_A, b = base + OFF_B + TILE * (i & 1);
+      bool ok = true;
+      auto issue_p = [&](int i) -> bool {   // P = a b^T once both landed
+        if (!wait_or_abort(bar_load + (i & 1), (i >> 1) & 1, abort)) return false;
+        const uint32_t a = base + STAGE * (i & 1) + OFF_A, b = base + STAGE * (i & 1) + OFF_B;
 #pragma unroll
         for (int kk = 0; kk < DA / 16; ++kk) {
           const uint32_t o = (kk >> 2) * 8192 + (kk & 3) * 32;
@@ -235,89 +246,142 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         mma_commit(bar_p);
         return true;
       };
-      if (nch > 0) {
-        if (!PHASE1) load_a(0);
-        load_b(0);
-        load_c(0);
-        if (nch > 1) {
-          load_b(1);
-          if (PHASE1) load_c(1);
-        }
-        if (!PHASE1) ok = issue_p(0);
-      }
+      if (!PHASE1 && nch > 0) ok = issue_p(0);
       for (int i = 0; ok && i < nch; ++i) {
-        const uint32_t ph = i & 1, ct = base + (PHASE1 && ph ? OFF_A : OFF_C);
-        const uint32_t term[3] = {base + OFF_B + TILE * ph, base + OFF_M, base + OFF_L};
-        // the chunk after the next: into L2, while the buffers it will land in are in use
-        if (!PHASE1 && i + 1 < nch)
-          for (int d = 0; d < DC / 64; ++d) tma_prefetch_4d(mc, 64 * d, hc, it.t0 + chunk_row(i + 1), it.b);
-        if (!PHASE1 && i + 2 < nch)
-          for (int d = 0; d < DA / 64; ++d) tma_prefetch_4d(ma, 64 * d, ha, it.t0 + chunk_row(i + 2), it.b);
-        if (!(ok = wait_or_abort(bar_ready, ph, abort))) break;
-        tc_fence_after();
-        if (!PHASE1) {   // O1^T = S^T a^T
-#pragma unroll
-          for (int kk = 0; kk < DA / 16; ++kk)
-            mma_ts(tmem + COL_O1, tmem + COL_S + 8 * kk, sdesc(base + OFF_A + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024),
-                   idesc_bf16(128, C, false, false), kk > 0);
-          mma_commit(bar_o1);
-        }
-        if (!(ok = wait_or_abort(bar_c + (PHASE1 ? ph : 0), PHASE1 ? (i >> 1) & 1 : ph, abort))) break;
+        const int st = i & 1;
+        const uint32_t sph = (i >> 1) & 1, sb = base + STAGE * st;
         // dS^T = c^T (w b)
+        if (!(ok = wait_or_abort(bar_load + st, sph, abort) && wait_or_abort(bar_ready + st, sph, abort))) break;
+        if (i > 0 && !(ok = wait_or_abort(bar_ds, (i - 1) & 1, abort))) break;
+        tc_fence_after();
+        const uint32_t term[3] = {sb + OFF_B, sb + OFF_M, sb + OFF_L};
 #pragma unroll
         for (int t = 0; t < 3; ++t)
           if (t < 2 || three)
 #pragma unroll
             for (int kk = 0; kk < C / 16; ++kk)
-              mma_ss(tmem + COL_DS, sdesc(ct + kk * 2048, 8192, 1024), sdesc(term[t] + kk * 2048, 8192, 1024),
+              mma_ss(tmem + COL_DS, sdesc(sb + OFF_C + kk * 2048, 8192, 1024), sdesc(term[t] + kk * 2048, 8192, 1024),
                      idesc_bf16(128, DA, true, true), t + kk > 0);
-        mma_commit(bar_kv);
-        if (!PHASE1) {
-          // O2^T = c^T P^T goes where S^T was read from: once O1^T is complete, while dS^T is under way
-          if (!(ok = wait_or_abort(bar_o1, ph, abort))) break;
+        mma_commit(bar_kv + st);
+        if (PHASE1) continue;
+        // the next chunk's P (this one's has been read)
+        if (i + 1 < nch && !(ok = issue_p(i + 1))) break;
+        // O1^T = S^T a^T, O2^T = c^T P^T
+        if (!(ok = wait_or_abort(bar_s, i & 1, abort))) break;
+        if (i >= 2 && !(ok = wait_or_abort(bar_oread + st, ((i - 2) >> 1) & 1, abort))) break;
+        tc_fence_after();
+        const uint32_t co = tmem + COL_O + 128 * st;
 #pragma unroll
-          for (int kk = 0; kk < C / 16; ++kk)
-            mma_ss(tmem + COL_O2, sdesc(ct + kk * 2048, 8192, 1024), sdesc(base + OFF_P + kk * 32, 16, 1024),
-                   idesc_bf16(128, C, true, false), kk > 0);
-          mma_commit(bar_o);
-          if (i + 1 < nch) load_a(i + 1);
-        }
-        if (!(ok = wait_or_abort(bar_kv, ph, abort))) break;
-        if (i + 2 < nch) {
-          load_b(i + 2);
-          if (PHASE1) load_c(i + 2);
-        }
-        if (!PHASE1 && i + 1 < nch) {
-          if (!(ok = wait_or_abort(bar_o, ph, abort))) break;
-          load_c(i + 1);
-          // P takes dS^T's columns once those are read
-          if (!(ok = wait_or_abort(bar_ds, ph, abort))) break;
-          tc_fence_after();
-          ok = issue_p(i + 1);
-        }
+        for (int kk = 0; kk < DA / 16; ++kk)
+          mma_ts(co, tmem + COL_S + 8 * kk, sdesc(sb + OFF_A + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024),
+                 idesc_bf16(128, C, false, false), kk > 0);
+#pragma unroll
+        for (int kk = 0; kk < C / 16; ++kk)
+          mma_ss(co + 64, sdesc(sb + OFF_C + kk * 2048, 8192, 1024), sdesc(sb + OFF_P + kk * 32, 16, 1024),
+                 idesc_bf16(128, C, true, false), kk > 0);
+        mma_commit(bar_o + st);
       }
-      if (!ok) {
-        // a wait gave up: report it, then let the MMAs and copies in flight finish
-        // (each wait again bounded) before shared and tensor memory are released
-        atomicOr(&g_gdr_linear_error, 1);
+      if (!ok) {   // a wait gave up: the MMAs in flight finish before the memory they use is released
         mma_commit(bar_drain);
         mbar_wait(bar_drain, 0);
-        if (issued_a) mbar_wait(bar_a, (issued_a - 1) & 1);
-        for (int b = 0; b < 2; ++b) {
-          const uint32_t nb = (issued_b + 1 - b) / 2, nc = PHASE1 ? (issued_c + 1 - b) / 2 : b ? 0 : issued_c;
-          if (nb) mbar_wait(bar_b + b, (nb - 1) & 1);
-          if (nc) mbar_wait(bar_c + b, (nc - 1) & 1);
-        }
       }
     }
+  } else if (warp >= NFINISH) {
+    // ---------------------------------------------------------------- prep: P and w b
+    const int quad = warp & 3, half = (warp - NFINISH) >> 2;
+    const int row = tid & 63, piece = (tid >> 6) & 3;   // w b: four threads per row
+    const float bscale = r.bscale;
+    const uint32_t lrow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    // P: rows t = 16 quad + lane / 4 (+ 8), columns s = 32 half + 8 j + 2 (lane % 4) (+ 1); the decays
+    // are the same for every chunk
+    uint64_t dec[4][2];
+    if (!PHASE1) {
+      const float f = bscale * r.yscale;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int t = 16 * quad + (lane >> 2) + 8 * k, s = 32 * half + 8 * j + 2 * (lane & 3);
+          const int d = rev ? s - t : t - s, d1 = rev ? d + 1 : d - 1;
+          dec[j][k] = pair_f32(d >= 0 ? f * pw[max(d, 0)] : 0.f, d1 >= 0 ? f * pw[max(d1, 0)] : 0.f);
+        }
+    }
+    const uint64_t minus_one = pair_f32(-1.f, -1.f);
+    for (int i = 0; i < nch; ++i) {
+      const int st = i & 1;
+      const uint32_t sph = (i >> 1) & 1;
+      uint8_t *sb = sm + STAGE * st;
+      const int n = min(C, end - chunk_row(i));
+      if (!__all_sync(0xffffffffu, wait_or_abort(bar_load + st, sph, abort))) break;
+      if (!PHASE1) {
+        if (!__all_sync(0xffffffffu, wait_or_abort(bar_p, i & 1, abort))) break;
+        tc_fence_after();
+        float v[16];
+        tmem_ld_frag4(lrow + COL_P + 32 * half, v);
+        tmem_wait_ld();
+        uint32_t u[4][2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float y0, y1;
+            unpair_f32(mul_f32x2(pair_f32(v[4 * j + 2 * k], v[4 * j + 2 * k + 1]), dec[j][k]), y0, y1);
+            if (n < C) {   // whatever lies behind the sequence's end has no part in this
+              const int s = 32 * half + 8 * j + 2 * (lane & 3);
+              y0 = s < n ? y0 : 0.f;
+              y1 = s + 1 < n ? y1 : 0.f;
+            }
+            u[j][k] = pack_bf16x2(y0, y1);
+          }
+        const int t = 16 * quad + (lane & 15), ch = 4 * half + (lane >> 4);
+        stmatrix4(smem_u32(sb + OFF_P + sw128(t, ch)), u[0][0], u[0][1], u[1][0], u[1][1]);
+        stmatrix4(smem_u32(sb + OFF_P + sw128(t, ch + 2)), u[2][0], u[2][1], u[3][0], u[3][1]);
+      }
+      if (row < n) {
+        const float w = pw[rev ? row + 1 : n - 1 - row] * bscale;
+        const uint64_t w2 = pair_f32(w, w);
+#pragma unroll
+        for (int jj = 0; jj < DA / 32; ++jj) {
+          const int j = piece * (DA / 32) + jj;
+          const uint32_t off = (j >> 3) * 8192 + sw128(row, j & 7);
+          uint4 v = *reinterpret_cast<const uint4 *>(sb + OFF_B + off), mid, lo;
+          split_pair(v.x, w2, minus_one, three, v.x, mid.x, lo.x);
+          split_pair(v.y, w2, minus_one, three, v.y, mid.y, lo.y);
+          split_pair(v.z, w2, minus_one, three, v.z, mid.z, lo.z);
+          split_pair(v.w, w2, minus_one, three, v.w, mid.w, lo.w);
+          *reinterpret_cast<uint4 *>(sb + OFF_B + off) = v;
+          *reinterpret_cast<uint4 *>(sb + OFF_M + off) = mid;
+          if (three) *reinterpret_cast<uint4 *>(sb + OFF_L + off) = lo;
+        }
+      } else {   // rows behind the sequence's end: zeros, in c too
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int jj = 0; jj < DA / 32; ++jj) {
+          const int j = piece * (DA / 32) + jj;
+          const uint32_t off = (j >> 3) * 8192 + sw128(row, j & 7);
+          *reinterpret_cast<uint4 *>(sb + OFF_B + off) = zero;
+          *reinterpret_cast<uint4 *>(sb + OFF_M + off) = zero;
+          *reinterpret_cast<uint4 *>(sb + OFF_L + off) = zero;
+        }
+#pragma unroll
+        for (int jj = 0; jj < DC / 32; ++jj) {
+          const int j = piece * (DC / 32) + jj;
+          *reinterpret_cast<uint4 *>(sb + OFF_C + (j >> 3) * 8192 + sw128(row, j & 7)) = zero;
+        }
+      }
+      fence_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_ready + st);
+    }
   } else {
-    // ---------------------------------------------------------------- compute warps
-    const int quad = warp & 3, half = warp >> 2;
-    const float bscale = r.bscale, yscale = r.yscale;
+    // ---------------------------------------------------------------- finish: the state and the outputs
+    const int quad = warp & 3, part = warp >> 2;
+    const float yscale = r.yscale;
     const bool y_f32 = r.y_f32 != 0;
-    // thread (quad, lane, half) holds S[da = half DA/2 + j][dc = 32 quad + lane], in pairs along da
-    constexpr int SN = DA / 2;
-    const int dcr = 32 * quad + lane, da0 = half * SN;
+    // thread (quad, lane, part) holds S[da = part DA/4 + j][dc = 32 quad + lane], in pairs along da
+    constexpr int SN = DA / 4;
+    const int dcr = 32 * quad + lane, da0 = part * SN;
     const bool has_c = dcr < DC;
     uint64_t S[SN / 2];
 #pragma unroll
@@ -348,105 +412,30 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     const uint32_t lrow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     ChunkDecay decay;
     decay.init(pw[C], pw_lo[C]);
-    auto store_operand = [&]() {   // S^T to tensor memory in bf16: columns da / 2
+    auto store_operand = [&]() {   // S^T to tensor memory in bf16 (columns da / 2), and the hand-over
+      uint32_t u[SN / 2];
 #pragma unroll
-      for (int q = 0; q < SN / 32; ++q) {
-        uint32_t u[16];
-#pragma unroll
-        for (int m = 0; m < 16; ++m) {
-          float a, b;
-          unpair_f32(S[16 * q + m], a, b);
-          u[m] = pack_bf16x2(a, b);
-        }
-        tmem_st16(lrow + COL_S + half * (SN / 2) + 16 * q, u);
+      for (int m = 0; m < SN / 2; ++m) {
+        float a, b;
+        unpair_f32(S[m], a, b);
+        u[m] = pack_bf16x2(a, b);
       }
+      if constexpr (SN == 32) tmem_st16(lrow + COL_S + part * 16, u);
+      else tmem_st8(lrow + COL_S + part * 8, u);
       tmem_wait_st();
-    };
-    if (!PHASE1) store_operand();
-
-    for (int i = 0; i < nch; ++i) {
-      const uint32_t ph = i & 1;
-      const int row0 = chunk_row(i), n = min(C, end - row0);
-      uint8_t *bt = sm + OFF_B + TILE * ph;
-
-      // 1. P with its decays, to bf16 (rows 16 quad .. of the M = 64 layout, columns 32 half ..)
-      if (!PHASE1) {
-        ok = __all_sync(0xffffffffu, wait_or_abort(bar_p, ph, abort));
-        if (!ok) break;
-        tc_fence_after();
-        float v[16];
-        tmem_ld_frag4(lrow + COL_P + 32 * half, v);
-        tmem_wait_ld();
-        uint32_t u[4][2];   // column groups of 8 x rows lane / 4 (+ 8)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int t = 16 * quad + (lane >> 2) + 8 * k, s = 32 * half + 8 * j + 2 * (lane & 3);
-            float y[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int d = rev ? s + e - t : t - s - e;
-              const float w = dtab[C + d];
-              y[e] = d >= 0 && s + e < n ? v[4 * j + 2 * k + e] * w : 0.f;
-            }
-            u[j][k] = pack_bf16x2(y[0], y[1]);
-          }
-        const int t = 16 * quad + (lane & 15), ch = 4 * half + (lane >> 4);
-        stmatrix4(smem_u32(sm + OFF_P + sw128(t, ch)), u[0][0], u[0][1], u[1][0], u[1][1]);
-        stmatrix4(smem_u32(sm + OFF_P + sw128(t, ch + 2)), u[2][0], u[2][1], u[3][0], u[3][1]);
-      }
-      // 2. w b in bf16 terms; rows behind the sequence's end become zeros, in c too
-      ok = __all_sync(0xffffffffu, wait_or_abort(bar_b + ph, (i >> 1) & 1, abort));
-      if (!ok) break;
-      {
-        const int row = tid & 63, piece = tid >> 6;   // four threads per row
-        if (row < n) {
-          const float w = pw[rev ? row + 1 : n - 1 - row] * bscale;
-          const uint64_t w2 = pair_f32(w, w), minus_one = pair_f32(-1.f, -1.f);
-#pragma unroll UNROLL_W
-          for (int jj = 0; jj < DA / 32; ++jj) {
-            const int j = piece * (DA / 32) + jj;
-            const uint32_t off = (j >> 3) * 8192 + sw128(row, j & 7);
-            uint4 v = *reinterpret_cast<const uint4 *>(bt + off), mid, lo;
-            split_pair(v.x, w2, minus_one, three, v.x, mid.x, lo.x);
-            split_pair(v.y, w2, minus_one, three, v.y, mid.y, lo.y);
-            split_pair(v.z, w2, minus_one, three, v.z, mid.z, lo.z);
-            split_pair(v.w, w2, minus_one, three, v.w, mid.w, lo.w);
-            *reinterpret_cast<uint4 *>(bt + off) = v;
-            *reinterpret_cast<uint4 *>(sm + OFF_M + off) = mid;
-            if (three) *reinterpret_cast<uint4 *>(sm + OFF_L + off) = lo;
-          }
-        }
-        if (n < C) {
-          ok = __all_sync(0xffffffffu, wait_or_abort(bar_c + (PHASE1 ? ph : 0), PHASE1 ? (i >> 1) & 1 : ph, abort));
-          if (!ok) break;
-          if (row >= n) {
-            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int jj = 0; jj < DA / 32; ++jj) {
-              const int j = piece * (DA / 32) + jj;
-              const uint32_t off = (j >> 3) * 8192 + sw128(row, j & 7);
-              *reinterpret_cast<uint4 *>(bt + off) = zero;
-              *reinterpret_cast<uint4 *>(sm + OFF_M + off) = zero;
-              *reinterpret_cast<uint4 *>(sm + OFF_L + off) = zero;
-            }
-#pragma unroll
-            for (int jj = 0; jj < DC / 32; ++jj) {
-              const int j = piece * (DC / 32) + jj;
-              *reinterpret_cast<uint4 *>(sm + (PHASE1 && ph ? OFF_A : OFF_C) + (j >> 3) * 8192 + sw128(row, j & 7)) = zero;
-            }
-          }
-        }
-      }
-      fence_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_ready);
-
-      // 3. S <- lambda^n S + dS
-      ok = __all_sync(0xffffffffu, wait_or_abort(bar_kv, ph, abort));
-      if (!ok) break;
+      if (lane == 0) mbar_arrive(bar_s);
+    };
+    if (!PHASE1) store_operand();
+    uint8_t *const stage = sm + OFF_Y + 1024 * warp;
+    bool ok = true;
+    for (int i = 0; i < nch; ++i) {
+      const int st = i & 1;
+      const uint32_t sph = (i >> 1) & 1;
+      const int row0 = chunk_row(i), n = min(C, end - row0);
+      // S <- lambda^n S + dS
+      if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar_kv + st, sph, abort)))) break;
       tc_fence_after();
       {
         const float g = n == C ? decay.next() : pw[n];
@@ -460,40 +449,45 @@ __global__ void __launch_bounds__(NTHREADS, 2)
           for (int e = 0; e < 8; ++e) S[8 * q + e] = fma_f32x2(g2, S[8 * q + e], pair_f32(v[2 * e], v[2 * e + 1]));
         }
       }
-      tc_fence_before();   // dS^T is read before the next product overwrites it
-      if (PHASE1) continue;
+      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_ds);
+      if (PHASE1) continue;
 
-      // 4. the output: this warp's 32 columns dc and 32 tokens t, through its 2 KB of
-      // shared memory (rows t of 64 bytes, 16-byte chunks XOR-ed with t / 2) unless in fp32
-      ok = __all_sync(0xffffffffu, wait_or_abort(bar_o, ph, abort));
-      if (!ok) break;
+      // its operand for the next chunk, once O1^T has been formed from this one's
+      if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar_o + st, sph, abort)))) break;
       tc_fence_after();
+      if (i + 1 < nch) store_operand();
+
+      // the output: this warp's 32 columns dc and 16 tokens t, through its 1 KB of
+      // shared memory (rows t of 64 bytes, 16-byte chunks XOR-ed with t / 2) unless in fp32
       if (quad * 32 < DC) {
-        uint8_t *stage = sm + OFF_M + 2048 * warp;
         const size_t y0 = ((static_cast<size_t>(it.b) * p.T + it.t0 + row0) * p.H + h) * DC + 32 * quad;
         const size_t ystep = static_cast<size_t>(p.H) * DC;
+        uint64_t g2[2];
 #pragma unroll
-        for (int qq = 0; qq < 4; ++qq) {   // 16 lanes of tensor memory x 16 columns: dc = 32 quad + 16 hh .., t = t0 ..
-          const int hh = qq & 1, t0 = 32 * half + 16 * (qq >> 1);
+        for (int j = 0; j < 2; ++j) {
+          const int t = 16 * part + 8 * j + 2 * (lane & 3);
+          g2[j] = pair_f32(yscale * pw[rev ? max(n - 1 - t, 0) : t + 1], yscale * pw[rev ? max(n - 2 - t, 0) : t + 2]);
+        }
+        if (!y_f32) __syncwarp();   // the rows of the chunk before have been read
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {   // 16 lanes of tensor memory: dc = 32 quad + 16 hh ..
           float v1[8], v2[8];
-          const uint32_t at = lrow + (static_cast<uint32_t>(16 * hh) << 16) + t0;
-          tmem_ld_frag2(at + COL_O1, v1);
-          tmem_ld_frag2(at + COL_O2, v2);
+          const uint32_t at = lrow + (static_cast<uint32_t>(16 * hh) << 16) + COL_O + 128 * st + 16 * part;
+          tmem_ld_frag2(at, v1);
+          tmem_ld_frag2(at + 64, v2);
           tmem_wait_ld();
           uint32_t u[2][2];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int t = t0 + 8 * j + 2 * (lane & 3);
-            const uint64_t g2 = pair_f32(yscale * pw[rev ? max(n - 1 - t, 0) : t + 1],
-                                         yscale * pw[rev ? max(n - 2 - t, 0) : t + 2]);
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               float ya, yb;
-              unpair_f32(fma_f32x2(g2, pair_f32(v1[4 * j + 2 * k], v1[4 * j + 2 * k + 1]),
+              unpair_f32(fma_f32x2(g2[j], pair_f32(v1[4 * j + 2 * k], v1[4 * j + 2 * k + 1]),
                                    pair_f32(v2[4 * j + 2 * k], v2[4 * j + 2 * k + 1])), ya, yb);
               if (y_f32) {
+                const int t = 16 * part + 8 * j + 2 * (lane & 3);
                 float *y = static_cast<float *>(r.y) + y0 + 16 * hh + 8 * k + (lane >> 2);
                 if (t < n) y[t * ystep] = ya;
                 if (t + 1 < n) y[(t + 1) * ystep] = yb;
@@ -501,29 +495,27 @@ __global__ void __launch_bounds__(NTHREADS, 2)
                 u[j][k] = pack_bf16x2(ya, yb);
               }
             }
-          }
           if (!y_f32) {
-            // matrix m: tokens t0 + 8 (m / 2) .., columns 16 hh + 8 (m & 1) ..; its row q = token
-            const int tt = 16 * (qq >> 1) + 8 * (lane >> 4) + (lane & 7), ch = 2 * hh + ((lane >> 3) & 1);
+            // matrix m: tokens 8 (m / 2) .., columns 16 hh + 8 (m & 1) ..; its row q = token
+            const int tt = 8 * (lane >> 4) + (lane & 7), ch = 2 * hh + ((lane >> 3) & 1);
             stmatrix4_trans(smem_u32(stage + tt * 64 + ((ch ^ (tt >> 1)) & 3) * 16), u[0][0], u[0][1], u[1][0], u[1][1]);
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_oread + st);
         if (!y_f32) {
-          __syncwarp();
           __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(r.y) + y0 + 8 * (lane & 3);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int tt = 8 * k + (lane >> 2), t = 32 * half + tt;
+          for (int k = 0; k < 2; ++k) {
+            const int tt = 8 * k + (lane >> 2), t = 16 * part + tt;
             const uint4 v = *reinterpret_cast<const uint4 *>(stage + tt * 64 + (((lane & 3) ^ (tt >> 1)) & 3) * 16);
             if (t < n) *reinterpret_cast<uint4 *>(y + t * ystep) = v;
           }
         }
+      } else if (lane == 0) {
+        mbar_arrive(bar_oread + st);
       }
-      // the quad's two warps share its lanes: O2^T is read by both before S^T replaces it, and
-      // the output rows lie where all warps write w b next
-      tc_fence_before();
-      named_bar_sync(1, 32 * NCOMPUTE);
-      if (i + 1 < nch) store_operand();
     }
     float *dst = PHASE1 ? r.X + (static_cast<size_t>(x) * p.H + h) * DA * DC : final_page;
     if (dst && has_c && ok) {
@@ -539,6 +531,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *abort) atomicOr(&g_gdr_linear_error, 1);
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
