@@ -26,7 +26,7 @@
 //
 // One CTA has the SM.  Its warps are specialised and hand over through
 // mbarriers, so that three chunks are under way at once:
-//     copies (1 warp)    a, b, c of chunk i + 2 into the stage that chunk i leaves
+//     copies (1 warp)    a, b, c of the chunks to come, each into the stage of one that is done
 //     prep   (8 warps)   P and w b of chunk i + 1
 //     MMAs   (1 warp)    dS(i), P(i + 1), O1(i), O2(i)
 //     finish (16 warps)  S after chunk i, its bf16 operand, the output rows of chunk i
@@ -47,24 +47,69 @@ constexpr int C = 64;
 constexpr int NFINISH = 16, NPREP = 8;   // warps 0 .. 15 and 16 .. 23, then the MMA and the copy warp
 constexpr int NTHREADS = 32 * (NFINISH + NPREP + 2);
 constexpr uint32_t TILE = 16384;        // 64 rows of two 128-byte atoms
-// one stage per chunk in flight
-constexpr uint32_t OFF_A = 0;
-constexpr uint32_t OFF_B = TILE;        // b; the first term of w b replaces it in place
-constexpr uint32_t OFF_C = 2 * TILE;
-constexpr uint32_t OFF_M = 3 * TILE;    // second and third terms of w b
-constexpr uint32_t OFF_L = 4 * TILE;
-constexpr uint32_t OFF_P = 5 * TILE;    // bf16 P, rows t, 8 KB
-constexpr uint32_t STAGE = OFF_P + 8192;
-constexpr uint32_t OFF_Y = 2 * STAGE;          // 1 KB of output rows per finishing warp
-constexpr uint32_t OFF_PW = OFF_Y + 1024 * NFINISH;   // lambda^0 .. lambda^64, then what fp32 loses of them
-constexpr uint32_t OFF_BAR = OFF_PW + 2 * 65 * 4 + 8;
-constexpr uint32_t SMEM_BYTES = OFF_BAR + 192 + 1024;
-static_assert(OFF_BAR % 16 == 0 && STAGE % 1024 == 0 && SMEM_BYTES <= 232448, "one CTA per SM");
+// Shared memory.  The copies run NST chunks ahead; what is made of a chunk has two
+// buffers (the third term of w b, with all runs' tensors in flight, one).
+template <bool PHASE1>
+struct Smem {
+  static constexpr int NST = PHASE1 ? 4 : 3;
+  static constexpr uint32_t B = 0;               // in a stage: b; the first term of w b replaces it in place
+  static constexpr uint32_t CT = TILE;
+  static constexpr uint32_t A = 2 * TILE;
+  static constexpr uint32_t STAGE = (PHASE1 ? 2 : 3) * TILE;
+  static constexpr uint32_t M = NST * STAGE;     // second term of w b, two buffers
+  static constexpr uint32_t L = M + 2 * TILE;    // third term
+  static constexpr int NL = PHASE1 ? 2 : 1;
+  static constexpr uint32_t P = L + NL * TILE;   // bf16 P, rows t, 8 KB, two buffers
+  static constexpr uint32_t Y = P + (PHASE1 ? 0 : 2 * 8192);      // 1 KB of output rows per finishing warp
+  static constexpr uint32_t PW = Y + (PHASE1 ? 0 : 1024 * NFINISH);   // lambda^0 .. lambda^64, then what fp32 loses of them
+  static constexpr uint32_t BAR = PW + 2 * 65 * 4 + 8;
+  static constexpr uint32_t BYTES = BAR + 208 + 1024;
+  static_assert(BAR % 16 == 0 && P % 1024 == 0 && BYTES <= 232448, "one CTA per SM");
+};
 constexpr uint32_t COL_DS = 0;     // dS^T, 128 columns
 constexpr uint32_t COL_S = 128;    // S^T in bf16, 64 columns
 constexpr uint32_t COL_P = 192;    // P, 64 columns
 constexpr uint32_t COL_O = 256;    // two buffers of O1^T and O2^T, 64 columns each
 constexpr uint32_t TMEM_COLS = 512;
+
+// Shared-memory matrix descriptors (sdesc()) in halves: `lo` of an address is followed by
+// that of an address o bytes on at + o / 16, so that the one thread that issues the MMAs
+// spends one addition on each (built from scratch they took it 100 cycles an MMA).
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);   // sbo 1024, version 1, SWIZZLE_128B
+template <bool ACC>
+__device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(alo), "r"(blo), "r"(idesc), "n"(ACC ? 1 : 0), "r"(DESC_HI)
+      : "memory");
+}
+template <bool ACC>
+__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(blo), "r"(idesc), "n"(ACC ? 1 : 0), "r"(DESC_HI)
+      : "memory");
+}
+// D (+)= A B over K steps of 16, A and B advancing by ao and bo bytes a step; steps
+// 4 .. 7 of a K-major operand lie in the next atom, 8 KB on.
+template <int STEPS, bool ACC0, bool A_ATOMS, bool B_ATOMS>
+__device__ __forceinline__ void mma_ss_steps(uint32_t d, uint32_t alo, uint32_t ao, uint32_t blo, uint32_t bo,
+                                             uint32_t idesc) {
+#pragma unroll
+  for (int kk = 0; kk < STEPS; ++kk) {
+    const uint32_t a = alo + (A_ATOMS ? (kk >> 2) * 512 + (kk & 3) * (ao / 16) : kk * (ao / 16));
+    const uint32_t b = blo + (B_ATOMS ? (kk >> 2) * 512 + (kk & 3) * (bo / 16) : kk * (bo / 16));
+    if (kk == 0) mma_ss_lo<ACC0>(d, a, b, idesc);
+    else mma_ss_lo<true>(d, a, b, idesc);
+  }
+}
 
 // Bounded wait that also gives up once another thread has.
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t phase, volatile int *abort) {
@@ -138,28 +183,35 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     return;
   }
 
-  float *pw = reinterpret_cast<float *>(sm + OFF_PW), *pw_lo = pw + 65;
-  // per stage (chunk i: barrier i & 1, phase (i >> 1) & 1)
-  uint64_t *bar_load = reinterpret_cast<uint64_t *>(sm + OFF_BAR);   // a, b and c landed
-  uint64_t *bar_ready = bar_load + 2;    // P and w b written (8 warps)
-  uint64_t *bar_kv = bar_load + 4;       // dS^T formed
-  uint64_t *bar_o = bar_load + 6;        // O1^T and O2^T formed
-  uint64_t *bar_oread = bar_load + 8;    // and read (16 warps)
+  using M = Smem<PHASE1>;
+  constexpr int NST = M::NST;
+  float *pw = reinterpret_cast<float *>(sm + M::PW), *pw_lo = pw + 65;
+  // per stage (chunk i: barrier i % NST, phase (i / NST) & 1)
+  uint64_t *bar_load = reinterpret_cast<uint64_t *>(sm + M::BAR);   // a, b and c landed
+  uint64_t *bar_free = bar_load + 4;     // every MMA that reads them complete
+  // per buffer (chunk i: barrier i & 1, phase (i >> 1) & 1)
+  uint64_t *bar_ready = bar_load + 8;    // P and w b written (8 warps)
+  uint64_t *bar_kv = bar_load + 10;      // dS^T formed
+  uint64_t *bar_o = bar_load + 12;       // O1^T and O2^T formed
+  uint64_t *bar_oread = bar_load + 14;   // and read (16 warps)
   // one each (chunk i: phase i & 1)
-  uint64_t *bar_p = bar_load + 10;       // P formed
-  uint64_t *bar_ds = bar_load + 11;      // dS^T read (16 warps)
-  uint64_t *bar_s = bar_load + 12;       // S^T of the chunk's start in tensor memory (16 warps)
-  uint64_t *bar_drain = bar_load + 13;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_load + 14);
-  volatile int *abort = reinterpret_cast<volatile int *>(bar_load + 15);
+  uint64_t *bar_p = bar_load + 16;       // P formed
+  uint64_t *bar_ds = bar_load + 17;      // dS^T read (16 warps)
+  uint64_t *bar_s = bar_load + 18;       // S^T of the chunk's start in tensor memory (16 warps)
+  uint64_t *bar_drain = bar_load + 19;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_load + 20);
+  volatile int *abort = reinterpret_cast<volatile int *>(bar_load + 21);
 
   if (warp == 0) {
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
   if (tid == 32) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NST; ++i) {
       mbar_init(bar_load + i, 1);
+      mbar_init(bar_free + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar_ready + i, NPREP);
       mbar_init(bar_kv + i, 1);
       mbar_init(bar_o + i, 1);
@@ -181,10 +233,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
   // value widths of 64: the upper 64 lanes of the M = 128 products read zeros
   if (DC == 64)
-    for (int i = tid; i < 512; i += NTHREADS) {
-      reinterpret_cast<uint4 *>(sm + OFF_C + 8192)[i] = make_uint4(0u, 0u, 0u, 0u);
-      reinterpret_cast<uint4 *>(sm + STAGE + OFF_C + 8192)[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
+    for (int i = tid; i < 512 * NST; i += NTHREADS)
+      reinterpret_cast<uint4 *>(sm + M::STAGE * (i >> 9) + M::CT + 8192)[i & 511] = make_uint4(0u, 0u, 0u, 0u);
   fence_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -209,17 +259,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       constexpr uint32_t bytes = (PHASE1 ? 0 : DA * 128) + DA * 128 + DC * 128;
       int i = 0;
       for (; i < nch; ++i) {
-        const int st = i & 1, row = it.t0 + chunk_row(i);
-        uint8_t *dst = sm + STAGE * st;
-        if (i >= 2 && !wait_or_abort((PHASE1 ? bar_kv : bar_o) + st, ((i - 2) >> 1) & 1, abort)) break;
+        const int st = i % NST, row = it.t0 + chunk_row(i);
+        uint8_t *dst = sm + M::STAGE * st;
+        if (i >= NST && !wait_or_abort(bar_free + st, (i / NST - 1) & 1, abort)) break;
         mbar_expect_tx(bar_load + st, bytes);
         for (int d = 0; d < DA / 64; ++d) {
-          tma_load_4d(dst + OFF_B + 8192 * d, mb, bar_load + st, 64 * d, hb, row, it.b);
-          if (!PHASE1) tma_load_4d(dst + OFF_A + 8192 * d, ma, bar_load + st, 64 * d, ha, row, it.b);
+          tma_load_4d(dst + M::B + 8192 * d, mb, bar_load + st, 64 * d, hb, row, it.b);
+          if (!PHASE1) tma_load_4d(dst + M::A + 8192 * d, ma, bar_load + st, 64 * d, ha, row, it.b);
         }
-        for (int d = 0; d < DC / 64; ++d) tma_load_4d(dst + OFF_C + 8192 * d, mc, bar_load + st, 64 * d, hc, row, it.b);
-        if (i + 2 < nch) {   // and the chunk that comes into this stage next, as far as L2
-          const int ahead = it.t0 + chunk_row(i + 2);
+        for (int d = 0; d < DC / 64; ++d) tma_load_4d(dst + M::CT + 8192 * d, mc, bar_load + st, 64 * d, hc, row, it.b);
+        if (i + NST < nch) {   // and the chunk that comes into this stage next, as far as L2
+          const int ahead = it.t0 + chunk_row(i + NST);
           for (int d = 0; d < DA / 64; ++d) {
             tma_prefetch_4d(mb, 64 * d, hb, ahead, it.b);
             if (!PHASE1) tma_prefetch_4d(ma, 64 * d, ha, ahead, it.b);
@@ -228,7 +278,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
       }
       // nothing may land in shared memory after the CTA (each wait bounded)
-      for (int j = i > 2 ? i - 2 : 0; j < i; ++j) mbar_wait(bar_load + (j & 1), (j >> 1) & 1);
+      for (int j = i > NST ? i - NST : 0; j < i; ++j) mbar_wait(bar_load + j % NST, (j / NST) & 1);
     }
   } else if (warp == NFINISH + NPREP) {
     // ---------------------------------------------------------------- MMAs
@@ -236,50 +286,51 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const uint32_t base = smem_u32(sm);
       bool ok = true;
       auto issue_p = [&](int i) -> bool {   // P = a b^T once both landed
-        if (!wait_or_abort(bar_load + (i & 1), (i >> 1) & 1, abort)) return false;
-        const uint32_t a = base + STAGE * (i & 1) + OFF_A, b = base + STAGE * (i & 1) + OFF_B;
-#pragma unroll
-        for (int kk = 0; kk < DA / 16; ++kk) {
-          const uint32_t o = (kk >> 2) * 8192 + (kk & 3) * 32;
-          mma_ss(tmem + COL_P, sdesc(a + o, 16, 1024), sdesc(b + o, 16, 1024), idesc_bf16(C, C, false, false), kk > 0);
-        }
+        if (!wait_or_abort(bar_load + i % NST, (i / NST) & 1, abort)) return false;
+        const uint32_t sb = base + M::STAGE * (i % NST);
+        mma_ss_steps<DA / 16, false, true, true>(tmem + COL_P, desc_lo(sb + M::A, 16), 32, desc_lo(sb + M::B, 16), 32,
+                                                 idesc_bf16(C, C, false, false));
         mma_commit(bar_p);
         return true;
       };
       if (!PHASE1 && nch > 0) ok = issue_p(0);
       for (int i = 0; ok && i < nch; ++i) {
-        const int st = i & 1;
-        const uint32_t sph = (i >> 1) & 1, sb = base + STAGE * st;
+        const int st = i % NST, bf = i & 1;
+        const uint32_t bph = (i >> 1) & 1, sb = base + M::STAGE * st;
+        const uint32_t clo = desc_lo(sb + M::CT, 8192);
         // dS^T = c^T (w b)
-        if (!(ok = wait_or_abort(bar_load + st, sph, abort) && wait_or_abort(bar_ready + st, sph, abort))) break;
+        if (!(ok = wait_or_abort(bar_load + st, (i / NST) & 1, abort) && wait_or_abort(bar_ready + bf, bph, abort))) break;
         if (i > 0 && !(ok = wait_or_abort(bar_ds, (i - 1) & 1, abort))) break;
         tc_fence_after();
-        const uint32_t term[3] = {sb + OFF_B, sb + OFF_M, sb + OFF_L};
-#pragma unroll
-        for (int t = 0; t < 3; ++t)
-          if (t < 2 || three)
-#pragma unroll
-            for (int kk = 0; kk < C / 16; ++kk)
-              mma_ss(tmem + COL_DS, sdesc(sb + OFF_C + kk * 2048, 8192, 1024), sdesc(term[t] + kk * 2048, 8192, 1024),
-                     idesc_bf16(128, DA, true, true), t + kk > 0);
-        mma_commit(bar_kv + st);
-        if (PHASE1) continue;
+        constexpr uint32_t id_kv = idesc_bf16(128, DA, true, true);
+        mma_ss_steps<C / 16, false, false, false>(tmem + COL_DS, clo, 2048, desc_lo(sb + M::B, 8192), 2048, id_kv);
+        mma_ss_steps<C / 16, true, false, false>(tmem + COL_DS, clo, 2048, desc_lo(base + M::M + TILE * bf, 8192), 2048,
+                                                 id_kv);
+        if (three)
+          mma_ss_steps<C / 16, true, false, false>(tmem + COL_DS, clo, 2048,
+                                                   desc_lo(base + M::L + TILE * (i % M::NL), 8192), 2048, id_kv);
+        mma_commit(bar_kv + bf);
+        if (PHASE1) {
+          mma_commit(bar_free + st);
+          continue;
+        }
         // the next chunk's P (this one's has been read)
         if (i + 1 < nch && !(ok = issue_p(i + 1))) break;
         // O1^T = S^T a^T, O2^T = c^T P^T
         if (!(ok = wait_or_abort(bar_s, i & 1, abort))) break;
-        if (i >= 2 && !(ok = wait_or_abort(bar_oread + st, ((i - 2) >> 1) & 1, abort))) break;
+        if (i >= 2 && !(ok = wait_or_abort(bar_oread + bf, ((i - 2) >> 1) & 1, abort))) break;
         tc_fence_after();
-        const uint32_t co = tmem + COL_O + 128 * st;
+        const uint32_t co = tmem + COL_O + 128 * bf, alo = desc_lo(sb + M::A, 16);
 #pragma unroll
-        for (int kk = 0; kk < DA / 16; ++kk)
-          mma_ts(co, tmem + COL_S + 8 * kk, sdesc(sb + OFF_A + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024),
-                 idesc_bf16(128, C, false, false), kk > 0);
-#pragma unroll
-        for (int kk = 0; kk < C / 16; ++kk)
-          mma_ss(co + 64, sdesc(sb + OFF_C + kk * 2048, 8192, 1024), sdesc(sb + OFF_P + kk * 32, 16, 1024),
-                 idesc_bf16(128, C, true, false), kk > 0);
-        mma_commit(bar_o + st);
+        for (int kk = 0; kk < DA / 16; ++kk) {
+          const uint32_t a = alo + (kk >> 2) * 512 + (kk & 3) * 2;
+          if (kk == 0) mma_ts_lo<false>(co, tmem + COL_S, a, idesc_bf16(128, C, false, false));
+          else mma_ts_lo<true>(co, tmem + COL_S + 8 * kk, a, idesc_bf16(128, C, false, false));
+        }
+        mma_ss_steps<C / 16, false, false, false>(co + 64, clo, 2048, desc_lo(base + M::P + 8192 * bf, 16), 32,
+                                                  idesc_bf16(128, C, true, false));
+        mma_commit(bar_o + bf);
+        mma_commit(bar_free + st);
       }
       if (!ok) {   // a wait gave up: the MMAs in flight finish before the memory they use is released
         mma_commit(bar_drain);
@@ -308,11 +359,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
     const uint64_t minus_one = pair_f32(-1.f, -1.f);
     for (int i = 0; i < nch; ++i) {
-      const int st = i & 1;
-      const uint32_t sph = (i >> 1) & 1;
-      uint8_t *sb = sm + STAGE * st;
+      const int st = i % NST, bf = i & 1;
+      uint8_t *sb = sm + M::STAGE * st, *mid_t = sm + M::M + TILE * bf, *lo_t = sm + M::L + TILE * (i % M::NL);
       const int n = min(C, end - chunk_row(i));
-      if (!__all_sync(0xffffffffu, wait_or_abort(bar_load + st, sph, abort))) break;
+      if (!__all_sync(0xffffffffu, wait_or_abort(bar_load + st, (i / NST) & 1, abort))) break;
+      // this chunk's buffers are those of the products of two chunks ago (a single third-term buffer: of
+      // the last one), which P's and b's arrival do not imply
+      if (i >= 2 && !__all_sync(0xffffffffu, wait_or_abort((PHASE1 ? bar_kv : bar_o) + bf, ((i - 2) >> 1) & 1, abort))) break;
+      if (M::NL == 1 && three && i >= 1 &&
+          !__all_sync(0xffffffffu, wait_or_abort(bar_kv + (bf ^ 1), ((i - 1) >> 1) & 1, abort))) break;
       if (!PHASE1) {
         if (!__all_sync(0xffffffffu, wait_or_abort(bar_p, i & 1, abort))) break;
         tc_fence_after();
@@ -334,8 +389,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             u[j][k] = pack_bf16x2(y0, y1);
           }
         const int t = 16 * quad + (lane & 15), ch = 4 * half + (lane >> 4);
-        stmatrix4(smem_u32(sb + OFF_P + sw128(t, ch)), u[0][0], u[0][1], u[1][0], u[1][1]);
-        stmatrix4(smem_u32(sb + OFF_P + sw128(t, ch + 2)), u[2][0], u[2][1], u[3][0], u[3][1]);
+        stmatrix4(smem_u32(sm + M::P + 8192 * bf + sw128(t, ch)), u[0][0], u[0][1], u[1][0], u[1][1]);
+        stmatrix4(smem_u32(sm + M::P + 8192 * bf + sw128(t, ch + 2)), u[2][0], u[2][1], u[3][0], u[3][1]);
       }
       if (row < n) {
         const float w = pw[rev ? row + 1 : n - 1 - row] * bscale;
@@ -344,14 +399,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (int jj = 0; jj < DA / 32; ++jj) {
           const int j = piece * (DA / 32) + jj;
           const uint32_t off = (j >> 3) * 8192 + sw128(row, j & 7);
-          uint4 v = *reinterpret_cast<const uint4 *>(sb + OFF_B + off), mid, lo;
+          uint4 v = *reinterpret_cast<const uint4 *>(sb + M::B + off), mid, lo;
           split_pair(v.x, w2, minus_one, three, v.x, mid.x, lo.x);
           split_pair(v.y, w2, minus_one, three, v.y, mid.y, lo.y);
           split_pair(v.z, w2, minus_one, three, v.z, mid.z, lo.z);
           split_pair(v.w, w2, minus_one, three, v.w, mid.w, lo.w);
-          *reinterpret_cast<uint4 *>(sb + OFF_B + off) = v;
-          *reinterpret_cast<uint4 *>(sb + OFF_M + off) = mid;
-          if (three) *reinterpret_cast<uint4 *>(sb + OFF_L + off) = lo;
+          *reinterpret_cast<uint4 *>(sb + M::B + off) = v;
+          *reinterpret_cast<uint4 *>(mid_t + off) = mid;
+          if (three) *reinterpret_cast<uint4 *>(lo_t + off) = lo;
         }
       } else {   // rows behind the sequence's end: zeros, in c too
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -359,20 +414,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (int jj = 0; jj < DA / 32; ++jj) {
           const int j = piece * (DA / 32) + jj;
           const uint32_t off = (j >> 3) * 8192 + sw128(row, j & 7);
-          *reinterpret_cast<uint4 *>(sb + OFF_B + off) = zero;
-          *reinterpret_cast<uint4 *>(sb + OFF_M + off) = zero;
-          *reinterpret_cast<uint4 *>(sb + OFF_L + off) = zero;
+          *reinterpret_cast<uint4 *>(sb + M::B + off) = zero;
+          *reinterpret_cast<uint4 *>(mid_t + off) = zero;
+          *reinterpret_cast<uint4 *>(lo_t + off) = zero;
         }
 #pragma unroll
         for (int jj = 0; jj < DC / 32; ++jj) {
           const int j = piece * (DC / 32) + jj;
-          *reinterpret_cast<uint4 *>(sb + OFF_C + (j >> 3) * 8192 + sw128(row, j & 7)) = zero;
+          *reinterpret_cast<uint4 *>(sb + M::CT + (j >> 3) * 8192 + sw128(row, j & 7)) = zero;
         }
       }
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_ready + st);
+      if (lane == 0) mbar_arrive(bar_ready + bf);
     }
   } else {
     // ---------------------------------------------------------------- finish: the state and the outputs
@@ -428,14 +483,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (lane == 0) mbar_arrive(bar_s);
     };
     if (!PHASE1) store_operand();
-    uint8_t *const stage = sm + OFF_Y + 1024 * warp;
+    uint8_t *const stage = sm + M::Y + 1024 * warp;
     bool ok = true;
     for (int i = 0; i < nch; ++i) {
-      const int st = i & 1;
-      const uint32_t sph = (i >> 1) & 1;
+      const int bf = i & 1;
+      const uint32_t bph = (i >> 1) & 1;
       const int row0 = chunk_row(i), n = min(C, end - row0);
       // S <- lambda^n S + dS
-      if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar_kv + st, sph, abort)))) break;
+      if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar_kv + bf, bph, abort)))) break;
       tc_fence_after();
       {
         const float g = n == C ? decay.next() : pw[n];
@@ -455,7 +510,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (PHASE1) continue;
 
       // its operand for the next chunk, once O1^T has been formed from this one's
-      if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar_o + st, sph, abort)))) break;
+      if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar_o + bf, bph, abort)))) break;
       tc_fence_after();
       if (i + 1 < nch) store_operand();
 
@@ -470,14 +525,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           const int t = 16 * part + 8 * j + 2 * (lane & 3);
           g2[j] = pair_f32(yscale * pw[rev ? max(n - 1 - t, 0) : t + 1], yscale * pw[rev ? max(n - 2 - t, 0) : t + 2]);
         }
-        if (!y_f32) __syncwarp();   // the rows of the chunk before have been read
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {   // 16 lanes of tensor memory: dc = 32 quad + 16 hh ..
           float v1[8], v2[8];
-          const uint32_t at = lrow + (static_cast<uint32_t>(16 * hh) << 16) + COL_O + 128 * st + 16 * part;
+          const uint32_t at = lrow + (static_cast<uint32_t>(16 * hh) << 16) + COL_O + 128 * bf + 16 * part;
           tmem_ld_frag2(at, v1);
           tmem_ld_frag2(at + 64, v2);
           tmem_wait_ld();
+          if (hh == 1) tc_fence_before();
+          __syncwarp();   // (the rows of the chunk before have been read from shared memory, too)
+          if (hh == 1 && lane == 0) mbar_arrive(bar_oread + bf);
           uint32_t u[2][2];
 #pragma unroll
           for (int j = 0; j < 2; ++j)
@@ -501,10 +558,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             stmatrix4_trans(smem_u32(stage + tt * 64 + ((ch ^ (tt >> 1)) & 3) * 16), u[0][0], u[0][1], u[1][0], u[1][1]);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_oread + st);
         if (!y_f32) {
+          __syncwarp();
           __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(r.y) + y0 + 8 * (lane & 3);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -514,7 +569,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
         }
       } else if (lane == 0) {
-        mbar_arrive(bar_oread + st);
+        mbar_arrive(bar_oread + bf);
       }
     }
     float *dst = PHASE1 ? r.X + (static_cast<size_t>(x) * p.H + h) * DA * DC : final_page;
@@ -540,13 +595,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
 template <int DA, int DC, bool PHASE1>
 cudaError_t launch(const LinProblem &p, const LinChunkMaps &maps, const LinRunSel &sel, bool pdl, cudaStream_t s) {
+  constexpr uint32_t SMEM = Smem<PHASE1>::BYTES;
   auto kern = linear_chunk_kernel<DA, DC, PHASE1>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long>(p.items) * p.H * sel.n));
   cfg.blockDim = dim3(NTHREADS);
-  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
