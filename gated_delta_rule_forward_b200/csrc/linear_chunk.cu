@@ -111,11 +111,24 @@ __device__ __forceinline__ void mma_ss_steps(uint32_t d, uint32_t alo, uint32_t 
   }
 }
 
-// Bounded wait that also gives up once another thread has.
+// Waits in the barrier's own time limit (about a millisecond), which leaves the issue
+// slots to the other warps; a loop of short ones took more of them than the arithmetic.
+__device__ __forceinline__ bool try_wait_long(uint64_t *bar, uint32_t phase) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(phase)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait (a second or so) that also gives up once another thread has.
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t phase, volatile int *abort) {
-  if (mbar_try_wait(bar, phase)) return true;
+  if (try_wait_long(bar, phase)) return true;
   const long long start = clock64();
-  while (!mbar_try_wait(bar, phase)) {
+  while (!try_wait_long(bar, phase)) {
     if (*abort) return false;
     if (clock64() - start > (1ll << 31)) {
       *abort = 1;
@@ -432,8 +445,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   } else {
     // ---------------------------------------------------------------- finish: the state and the outputs
     const int quad = warp & 3, part = warp >> 2;
-    const float yscale = r.yscale;
-    const bool y_f32 = r.y_f32 != 0;
     // thread (quad, lane, part) holds S[da = part DA/4 + j][dc = 32 quad + lane], in pairs along da
     constexpr int SN = DA / 4;
     const int dcr = 32 * quad + lane, da0 = part * SN;
@@ -483,12 +494,40 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (lane == 0) mbar_arrive(bar_s);
     };
     if (!PHASE1) store_operand();
-    uint8_t *const stage = sm + M::Y + 1024 * warp;
+    // the output: this warp's 32 columns dc and 16 tokens t, through its 1 KB of shared
+    // memory (rows t of 64 bytes, 16-byte chunks XOR-ed with t / 2) unless in fp32.
+    // Fragment tiles: lane holds dc = 16 hh + lane / 4 (+ 8), t = 8 j + 2 (lane % 4) (+ 1).
+    const bool has_y = !PHASE1 && quad * 32 < DC, y_f32 = r.y_f32 != 0;
+    const float yscale = r.yscale;
+    const size_t ystep = static_cast<size_t>(p.H) * DC;
+    const int tf = 16 * part + 2 * (lane & 3), tr = 16 * part + (lane >> 2);
+    const uint32_t stage = smem_u32(sm + M::Y + 1024 * warp);
+    // stmatrix: matrix m = tokens 8 (m / 2) .., columns 8 (m & 1) ..; its row q = token
+    const int tq = 8 * (lane >> 4) + (lane & 7), cq = (lane >> 3) & 1;
+    const uint32_t put0 = stage + tq * 64 + (((cq ^ (tq >> 1)) & 3) << 4), put1 = stage + tq * 64 + ((((2 + cq) ^ (tq >> 1)) & 3) << 4);
+    const uint32_t get = stage + (lane >> 2) * 64 + ((((lane & 3) ^ (lane >> 3)) & 3) << 4);   // and 512 bytes on: token + 8
+    // row tr's address in this chunk, advanced chunk by chunk; full chunks' decays
+    uint8_t *yrow = nullptr;
+    const long long yadvance = (rev ? -C : C) * static_cast<long long>(ystep) * (y_f32 ? 4 : 2);
+    uint64_t gam[2] = {0, 0};
+    auto gamma = [&](int n, uint64_t (&g)[2]) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int t = tf + 8 * j;
+        g[j] = pair_f32(yscale * pw[rev ? max(n - 1 - t, 0) : t + 1], yscale * pw[rev ? max(n - 2 - t, 0) : t + 2]);
+      }
+    };
+    if (has_y && nch > 0) {
+      const size_t row = static_cast<size_t>(it.b) * p.T + it.t0 + chunk_row(0);
+      if (y_f32) yrow = reinterpret_cast<uint8_t *>(static_cast<float *>(r.y) + (row + tf) * ystep + h * DC + 32 * quad + (lane >> 2));
+      else yrow = reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(r.y) + (row + tr) * ystep + h * DC + 32 * quad + 8 * (lane & 3));
+      gamma(C, gam);
+    }
     bool ok = true;
     for (int i = 0; i < nch; ++i) {
       const int bf = i & 1;
       const uint32_t bph = (i >> 1) & 1;
-      const int row0 = chunk_row(i), n = min(C, end - row0);
+      const int n = min(C, end - chunk_row(i));
       // S <- lambda^n S + dS
       if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar_kv + bf, bph, abort)))) break;
       tc_fence_after();
@@ -513,64 +552,70 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar_o + bf, bph, abort)))) break;
       tc_fence_after();
       if (i + 1 < nch) store_operand();
-
-      // the output: this warp's 32 columns dc and 16 tokens t, through its 1 KB of
-      // shared memory (rows t of 64 bytes, 16-byte chunks XOR-ed with t / 2) unless in fp32
-      if (quad * 32 < DC) {
-        const size_t y0 = ((static_cast<size_t>(it.b) * p.T + it.t0 + row0) * p.H + h) * DC + 32 * quad;
-        const size_t ystep = static_cast<size_t>(p.H) * DC;
-        uint64_t g2[2];
+      if (!has_y) {
+        if (lane == 0) mbar_arrive(bar_oread + bf);
+        continue;
+      }
+      if (n < C) gamma(n, gam);
+      const uint32_t col = lrow + COL_O + 128 * bf + 16 * part;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int t = 16 * part + 8 * j + 2 * (lane & 3);
-          g2[j] = pair_f32(yscale * pw[rev ? max(n - 1 - t, 0) : t + 1], yscale * pw[rev ? max(n - 2 - t, 0) : t + 2]);
+      for (int hh = 0; hh < 2; ++hh) {   // 16 lanes of tensor memory: dc = 32 quad + 16 hh ..
+        float v1[8], v2[8];
+        const uint32_t at = col + (static_cast<uint32_t>(16 * hh) << 16);
+        tmem_ld_frag2(at, v1);
+        tmem_ld_frag2(at + 64, v2);
+        tmem_wait_ld();
+        if (hh == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_oread + bf);
         }
+        uint64_t y[2][2];
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {   // 16 lanes of tensor memory: dc = 32 quad + 16 hh ..
-          float v1[8], v2[8];
-          const uint32_t at = lrow + (static_cast<uint32_t>(16 * hh) << 16) + COL_O + 128 * bf + 16 * part;
-          tmem_ld_frag2(at, v1);
-          tmem_ld_frag2(at + 64, v2);
-          tmem_wait_ld();
-          if (hh == 1) tc_fence_before();
-          __syncwarp();   // (the rows of the chunk before have been read from shared memory, too)
-          if (hh == 1 && lane == 0) mbar_arrive(bar_oread + bf);
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            y[j][k] = fma_f32x2(gam[j], pair_f32(v1[4 * j + 2 * k], v1[4 * j + 2 * k + 1]),
+                                pair_f32(v2[4 * j + 2 * k], v2[4 * j + 2 * k + 1]));
+        float a, b;
+        if (y_f32) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float *dst = reinterpret_cast<float *>(yrow) + 8 * j * ystep + 16 * hh + 8 * k;
+              unpair_f32(y[j][k], a, b);
+              if (tf + 8 * j < n) dst[0] = a;
+              if (tf + 8 * j + 1 < n) dst[ystep] = b;
+            }
+        } else {
           uint32_t u[2][2];
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              float ya, yb;
-              unpair_f32(fma_f32x2(g2[j], pair_f32(v1[4 * j + 2 * k], v1[4 * j + 2 * k + 1]),
-                                   pair_f32(v2[4 * j + 2 * k], v2[4 * j + 2 * k + 1])), ya, yb);
-              if (y_f32) {
-                const int t = 16 * part + 8 * j + 2 * (lane & 3);
-                float *y = static_cast<float *>(r.y) + y0 + 16 * hh + 8 * k + (lane >> 2);
-                if (t < n) y[t * ystep] = ya;
-                if (t + 1 < n) y[(t + 1) * ystep] = yb;
-              } else {
-                u[j][k] = pack_bf16x2(ya, yb);
-              }
+              unpair_f32(y[j][k], a, b);
+              u[j][k] = pack_bf16x2(a, b);
             }
-          if (!y_f32) {
-            // matrix m: tokens 8 (m / 2) .., columns 16 hh + 8 (m & 1) ..; its row q = token
-            const int tt = 8 * (lane >> 4) + (lane & 7), ch = 2 * hh + ((lane >> 3) & 1);
-            stmatrix4_trans(smem_u32(stage + tt * 64 + ((ch ^ (tt >> 1)) & 3) * 16), u[0][0], u[0][1], u[1][0], u[1][1]);
-          }
+          stmatrix4_trans(hh ? put1 : put0, u[0][0], u[0][1], u[1][0], u[1][1]);
         }
-        if (!y_f32) {
-          __syncwarp();
-          __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(r.y) + y0 + 8 * (lane & 3);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int tt = 8 * k + (lane >> 2), t = 16 * part + tt;
-            const uint4 v = *reinterpret_cast<const uint4 *>(stage + tt * 64 + (((lane & 3) ^ (tt >> 1)) & 3) * 16);
-            if (t < n) *reinterpret_cast<uint4 *>(y + t * ystep) = v;
-          }
-        }
-      } else if (lane == 0) {
-        mbar_arrive(bar_oread + bf);
       }
+      if (!y_f32) {
+        __syncwarp();
+        uint4 v0, v1;
+        ld_shared_v4(get, v0);
+        ld_shared_v4(get + 512, v1);
+        if (n == C) {
+          *reinterpret_cast<uint4 *>(yrow) = v0;
+          *reinterpret_cast<uint4 *>(yrow + 16 * ystep) = v1;
+        } else {
+          if (tr < n) *reinterpret_cast<uint4 *>(yrow) = v0;
+          if (tr + 8 < n) *reinterpret_cast<uint4 *>(yrow + 16 * ystep) = v1;
+        }
+        __syncwarp();   // read before the next chunk's rows are put there
+      }
+      if (n < C) gamma(C, gam);
+      yrow += yadvance;
     }
     float *dst = PHASE1 ? r.X + (static_cast<size_t>(x) * p.H + h) * DA * DC : final_page;
     if (dst && has_c && ok) {

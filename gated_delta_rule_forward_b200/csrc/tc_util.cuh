@@ -337,6 +337,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ void ld_shared_v4(uint32_t saddr, uint4 &v) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(saddr));
+}
+
 // Two fp32 values in one register pair, and the paired instructions on them.
 __device__ __forceinline__ uint64_t pair_f32(float a, float b) {
   uint64_t r;
