@@ -11,9 +11,9 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // Start states from the segments' end states, in place: per element and
-// sequence X_g <- S_g, S_{g+1} = lambda^{len_g} S_g + X_g.  The loads of
-// several segments are issued together; only the fused multiply-adds depend
-// on one another.
+// sequence X_g <- S_g, S_{g+1} = lambda^{len_g} S_g + X_g, and the state after the
+// last segment where it is wanted.  The loads of several segments are issued
+// together; only the fused multiply-adds depend on one another.
 constexpr int kChainThreads = 256;
 
 __global__ void __launch_bounds__(kChainThreads) linear_chain_kernel(const LinProblem p) {
@@ -51,25 +51,28 @@ __global__ void __launch_bounds__(kChainThreads) linear_chain_kernel(const LinPr
     }
     const size_t step = static_cast<size_t>(p.H) * page_elems / 4;
     float4 *X = reinterpret_cast<float4 *>(r.X) + (static_cast<size_t>(x0) * p.H + h) * (page_elems / 4) + e4;
+    float4 *fin = r.s_final && page >= 0 ? reinterpret_cast<float4 *>(
+        r.s_final + (static_cast<size_t>(page) * p.H + h) * page_elems) + e4 : nullptr;
     constexpr int U = 8;
     for (int i0 = 0; i0 < nseg; i0 += U) {
       float4 d[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (i0 + u < nseg - 1) d[u] = X[(r.reverse ? nseg - 1 - (i0 + u) : i0 + u) * step];
+        if (i0 + u < nseg - (fin ? 0 : 1)) d[u] = X[(r.reverse ? nseg - 1 - (i0 + u) : i0 + u) * step];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = i0 + u;
         if (i >= nseg) break;
         X[(r.reverse ? nseg - 1 - i : i) * step] = cur;
-        if (i == nseg - 1) break;
-        const float f = r.reverse && i == 0 ? ftail : full;
+        if (i == nseg - 1 && !fin) break;
+        const float f = i == (r.reverse ? 0 : nseg - 1) ? ftail : full;   // the sequence's last segment may be short
         cur.x = fmaf(f, cur.x, d[u].x);
         cur.y = fmaf(f, cur.y, d[u].y);
         cur.z = fmaf(f, cur.z, d[u].z);
         cur.w = fmaf(f, cur.w, d[u].w);
       }
     }
+    if (fin) *fin = cur;
   }
 }
 

@@ -7,18 +7,20 @@
 //     S <- lambda^n S + bscale sum_s w_s b_s c_s^T,
 //     forward: Gamma_t = lambda^{t+1}, w_s = lambda^{n-1-s};  reverse: the two exchanged.
 // One CTA sweeps the chunks of one (run, segment, head) in order; everything is
-// held transposed, so that M = 128 of the MMAs is the value width and the state
-// is their tensor-memory operand:
-//     P    [t][s]   = a b^T          M64  N64  K = da   (tensor memory)
-//     dS^T [dc][da] = c^T (w b)      M128 N = da, K = 64
-//     O1^T [dc][t]  = S^T a^T        M128 N64  K = da   (S^T in bf16 in tensor memory)
+// held transposed, so that M = 128 of the MMAs is the value width and both the
+// state and the weighted values are tensor-memory operands:
+//     P    [t][s]   = a b^T          M64  N64  K = da   (into tensor memory)
+//     dS^T [dc][da] = (w c)^T b      M128 N = da, K = 64
+//     O1^T [dc][t]  = S^T a^T        M128 N64  K = da
 //     O2^T [dc][t]  = c^T P^T        M128 N64  K = 64   (P back through shared memory in bf16)
 // and Y^T = yscale (Gamma_t O1^T + O2^T).  The fp32 state lives in registers of
 // 16 warps: lane dc of a quad, a quarter of da per thread; S <- lambda^n S + dS
-// is one pass over it.
+// is one pass over it.  What bounds the sweep on the chip is the 128 bytes a clock
+// of shared memory: weighting c on its way into tensor memory, rather than b in
+// place, takes 64 KB of a chunk's 272 KB off it.
 //
-// Rounding.  The products' inputs are exact bf16 except three: w b, P and the
-// S^T operand.  w b enters the state, which is fp32, so it is split into three
+// Rounding.  The products' inputs are exact bf16 except three: w c, P and the
+// S^T operand.  w c enters the state, which is fp32, so it is split into three
 // bf16 terms (24 bits, three MMAs): the state keeps fp32 accuracy; where the
 // state is not kept (a later segment starts from phase 1's), two terms do, 2^-8
 // of what follows.  P and S^T enter only Y, on disjoint parts of its sum, and
@@ -27,10 +29,12 @@
 // One CTA has the SM.  Its warps are specialised and hand over through
 // mbarriers, so that three chunks are under way at once:
 //     copies (1 warp)    a, b, c of the chunks to come, each into the stage of one that is done
-//     prep   (8 warps)   P and w b of chunk i + 1
+//     prep   (8 warps)   P and w c of chunk i + 1
 //     MMAs   (1 warp)    dS(i), P(i + 1), O1(i), O2(i)
 //     finish (16 warps)  S after chunk i, its bf16 operand, the output rows of chunk i
 // Only S -> operand -> O1 is a chain from chunk to chunk.
+#include <type_traits>
+
 #include "linear.cuh"
 #include "linear_chunk.cuh"
 #include "tc_util.cuh"
@@ -47,96 +51,151 @@ constexpr int C = 64;
 constexpr int NFINISH = 16, NPREP = 8;   // warps 0 .. 15 and 16 .. 23, then the MMA and the copy warp
 constexpr int NTHREADS = 32 * (NFINISH + NPREP + 2);
 constexpr uint32_t TILE = 16384;        // 64 rows of two 128-byte atoms
-// Shared memory.  The copies run NST chunks ahead; what is made of a chunk has two
-// buffers (the third term of w b, with all runs' tensors in flight, one).
+// Shared memory.  The copies run NST chunks ahead.
 template <bool PHASE1>
 struct Smem {
-  static constexpr int NST = PHASE1 ? 4 : 3;
-  static constexpr uint32_t B = 0;               // in a stage: b; the first term of w b replaces it in place
+  static constexpr int NST = PHASE1 ? 6 : 4;
+  static constexpr uint32_t B = 0;               // in a stage
   static constexpr uint32_t CT = TILE;
   static constexpr uint32_t A = 2 * TILE;
   static constexpr uint32_t STAGE = (PHASE1 ? 2 : 3) * TILE;
-  static constexpr uint32_t M = NST * STAGE;     // second term of w b, two buffers
-  static constexpr uint32_t L = M + 2 * TILE;    // third term
-  static constexpr int NL = PHASE1 ? 2 : 1;
-  static constexpr uint32_t P = L + NL * TILE;   // bf16 P, rows t, 8 KB, two buffers
+  static constexpr uint32_t P = NST * STAGE;     // bf16 P, rows t, 8 KB, two buffers
   static constexpr uint32_t Y = P + (PHASE1 ? 0 : 2 * 8192);      // 1 KB of output rows per finishing warp
   static constexpr uint32_t PW = Y + (PHASE1 ? 0 : 1024 * NFINISH);   // lambda^0 .. lambda^64, then what fp32 loses of them
   static constexpr uint32_t BAR = PW + 2 * 65 * 4 + 8;
-  static constexpr uint32_t BYTES = BAR + 208 + 1024;
+  // barriers per stage
+  static constexpr uint32_t LOAD = BAR;              // a, b and c landed
+  static constexpr uint32_t FREE = LOAD + 8 * NST;   // every MMA that reads them complete
+  // per buffer of two
+  static constexpr uint32_t READY = FREE + 8 * NST;  // P and w c written (8 warps)
+  static constexpr uint32_t KV = READY + 16;         // dS^T formed
+  static constexpr uint32_t OUT = KV + 16;           // O1^T and O2^T formed
+  // one each
+  static constexpr uint32_t OREAD = OUT + 16;        // O1^T and O2^T read (16 warps)
+  static constexpr uint32_t PF = OREAD + 8;          // P formed
+  static constexpr uint32_t PREAD = PF + 8;          // P read (8 warps)
+  static constexpr uint32_t DS = PREAD + 8;          // dS^T read (16 warps)
+  static constexpr uint32_t SOP = DS + 8;            // S^T of the chunk's start in tensor memory (16 warps)
+  static constexpr uint32_t DRAIN = SOP + 8;
+  static constexpr uint32_t SLOT = DRAIN + 8;        // tensor-memory address
+  static constexpr uint32_t ABORT = SLOT + 4;        // a wait gave up
+  static constexpr uint32_t BYTES = ABORT + 4 + 1024;
   static_assert(BAR % 16 == 0 && P % 1024 == 0 && BYTES <= 232448, "one CTA per SM");
 };
-constexpr uint32_t COL_DS = 0;     // dS^T, 128 columns
-constexpr uint32_t COL_S = 128;    // S^T in bf16, 64 columns
-constexpr uint32_t COL_P = 192;    // P, 64 columns
-constexpr uint32_t COL_O = 256;    // two buffers of O1^T and O2^T, 64 columns each
+// Tensor memory columns.
+template <bool PHASE1>
+struct Tmem {
+  static constexpr uint32_t DS = 0;      // dS^T, 128
+  static constexpr uint32_t S = 128;     // S^T in bf16, 64
+  static constexpr uint32_t P = 192;     // P, 64
+  static constexpr uint32_t O = 256;     // O1^T and O2^T, 64 each
+  // (w c)^T in bf16, 32 columns a term: two buffers of two terms (phase 1: of three);
+  // beside the outputs there is room for one buffer of three
+  static constexpr uint32_t W = PHASE1 ? 128 : 384;
+  __device__ static constexpr uint32_t term(int buf, int t) { return W + (PHASE1 ? 128 : 64) * buf + 32 * t; }
+};
 constexpr uint32_t TMEM_COLS = 512;
 
-// Shared-memory matrix descriptors (sdesc()) in halves: `lo` of an address is followed by
-// that of an address o bytes on at + o / 16, so that the one thread that issues the MMAs
-// spends one addition on each (built from scratch they took it 100 cycles an MMA).
+// The MMAs are issued by the lane that elect.sync picks, with the predicate inside the
+// instruction and everything around it done by the whole warp: descriptors then stay in
+// uniform registers, and an issue takes 26 cycles (measured, M64 N64) where the same
+// instruction inside `if (lane == 0)` takes 50 to 100, more than it executes.  Descriptors
+// (sdesc()) come in halves: `lo` of an address is followed by that of an address o bytes
+// on at + o / 16.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
 constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);   // sbo 1024, version 1, SWIZZLE_128B
 template <bool ACC>
-__device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc) {
+__device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t e) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
       "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(alo), "r"(blo), "r"(idesc), "n"(ACC ? 1 : 0), "r"(DESC_HI)
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(alo), "r"(blo), "r"(idesc), "n"(ACC ? 1 : 0), "r"(DESC_HI), "r"(e)
       : "memory");
 }
 template <bool ACC>
-__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t idesc) {
+__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t idesc, uint32_t e) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
       "mov.b64 b, {%2, %5};\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(blo), "r"(idesc), "n"(ACC ? 1 : 0), "r"(DESC_HI)
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(blo), "r"(idesc), "n"(ACC ? 1 : 0), "r"(DESC_HI), "r"(e)
       : "memory");
 }
-// D (+)= A B over K steps of 16, A and B advancing by ao and bo bytes a step; steps
-// 4 .. 7 of a K-major operand lie in the next atom, 8 KB on.
-template <int STEPS, bool ACC0, bool A_ATOMS, bool B_ATOMS>
-__device__ __forceinline__ void mma_ss_steps(uint32_t d, uint32_t alo, uint32_t ao, uint32_t blo, uint32_t bo,
-                                             uint32_t idesc) {
-#pragma unroll
-  for (int kk = 0; kk < STEPS; ++kk) {
-    const uint32_t a = alo + (A_ATOMS ? (kk >> 2) * 512 + (kk & 3) * (ao / 16) : kk * (ao / 16));
-    const uint32_t b = blo + (B_ATOMS ? (kk >> 2) * 512 + (kk & 3) * (bo / 16) : kk * (bo / 16));
-    if (kk == 0) mma_ss_lo<ACC0>(d, a, b, idesc);
-    else mma_ss_lo<true>(d, a, b, idesc);
-  }
+__device__ __forceinline__ void commit_one(uint32_t bar, uint32_t e) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(e)
+      : "memory");
 }
 
-// Waits in the barrier's own time limit (about a millisecond), which leaves the issue
-// slots to the other warps; a loop of short ones took more of them than the arithmetic.
-__device__ __forceinline__ bool try_wait_long(uint64_t *bar, uint32_t phase) {
+// Barriers by their 32-bit shared-memory addresses: with 24 warps waiting and arriving
+// several times a chunk, generic pointers cost more integer instructions than the
+// arithmetic took.
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void expect_at(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Waits up to the given limit (a millisecond), which leaves the issue slots to others.
+__device__ __forceinline__ bool try_wait_at(uint32_t bar, uint32_t phase) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(phase)
+      : "r"(bar), "r"(phase)
       : "memory");
   return ok != 0;
 }
-// Bounded wait (a second or so) that also gives up once another thread has.
-__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t phase, volatile int *abort) {
-  if (try_wait_long(bar, phase)) return true;
+// Bounded wait (a second or so) that also gives up once another thread has (the word at
+// `abort`).
+__device__ __forceinline__ bool wait_at(uint32_t bar, uint32_t phase, uint32_t abort) {
+  if (try_wait_at(bar, phase)) return true;
   const long long start = clock64();
-  while (!try_wait_long(bar, phase)) {
-    if (*abort) return false;
+  while (!try_wait_at(bar, phase)) {
+    uint32_t gave_up;
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(gave_up) : "r"(abort) : "memory");
+    if (gave_up) return false;
     if (clock64() - start > (1ll << 31)) {
-      *abort = 1;
+      asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
       return false;
     }
   }
   return true;
 }
+// The same by a whole warp.
+__device__ __forceinline__ bool warp_wait_at(uint32_t bar, uint32_t phase, uint32_t abort) {
+  return __all_sync(0xffffffffu, wait_at(bar, phase, abort));
+}
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+// A ring of N barriers or stages: index and phase of one chunk after another.
+template <int N>
+struct Ring {
+  uint32_t at = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
 
 // lambda^64 as one of the two fp32 values beside it, chosen chunk by chunk so that their
 // running product stays within a rounding of the exact power: one fixed value's rounding,
@@ -161,8 +220,9 @@ struct ChunkDecay {
 
 // w x of two bf16 values x as a sum of bf16 pairs: two terms keep 16 significant bits,
 // three keep 24.
-__device__ __forceinline__ void split_pair(uint32_t x, uint64_t w, uint64_t minus_one, bool three, uint32_t &hi,
-                                           uint32_t &mid, uint32_t &lo) {
+template <int TERMS>
+__device__ __forceinline__ void split_pair(uint32_t x, uint64_t w, uint64_t minus_one, uint32_t &hi, uint32_t &mid,
+                                           uint32_t &lo) {
   const uint64_t p = mul_f32x2(pair_f32(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), w);
   float a, b;
   unpair_f32(p, a, b);
@@ -170,7 +230,7 @@ __device__ __forceinline__ void split_pair(uint32_t x, uint64_t w, uint64_t minu
   const uint64_t r = fma_f32x2(pair_f32(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)), minus_one, p);
   unpair_f32(r, a, b);
   mid = pack_bf16x2(a, b);
-  if (three) {
+  if (TERMS == 3) {
     unpair_f32(fma_f32x2(pair_f32(__uint_as_float(mid << 16), __uint_as_float(mid & 0xffff0000u)), minus_one, r), a, b);
     lo = pack_bf16x2(a, b);
   }
@@ -190,51 +250,38 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const bool rev = r.reverse != 0;
   const LinItem it = lin_item(p, x);
   const bool last = rev ? it.g == 0 : it.g == it.nseg - 1;   // in the run's order
-  if (!it.ok || (PHASE1 && last)) {
+  if (!it.ok || (PHASE1 && last && (it.nseg == 1 || !r.s_final))) {
     griddep_launch_dependents();
     griddep_wait();
     return;
   }
 
   using M = Smem<PHASE1>;
+  using T = Tmem<PHASE1>;
   constexpr int NST = M::NST;
   float *pw = reinterpret_cast<float *>(sm + M::PW), *pw_lo = pw + 65;
-  // per stage (chunk i: barrier i % NST, phase (i / NST) & 1)
-  uint64_t *bar_load = reinterpret_cast<uint64_t *>(sm + M::BAR);   // a, b and c landed
-  uint64_t *bar_free = bar_load + 4;     // every MMA that reads them complete
-  // per buffer (chunk i: barrier i & 1, phase (i >> 1) & 1)
-  uint64_t *bar_ready = bar_load + 8;    // P and w b written (8 warps)
-  uint64_t *bar_kv = bar_load + 10;      // dS^T formed
-  uint64_t *bar_o = bar_load + 12;       // O1^T and O2^T formed
-  uint64_t *bar_oread = bar_load + 14;   // and read (16 warps)
-  // one each (chunk i: phase i & 1)
-  uint64_t *bar_p = bar_load + 16;       // P formed
-  uint64_t *bar_ds = bar_load + 17;      // dS^T read (16 warps)
-  uint64_t *bar_s = bar_load + 18;       // S^T of the chunk's start in tensor memory (16 warps)
-  uint64_t *bar_drain = bar_load + 19;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_load + 20);
-  volatile int *abort = reinterpret_cast<volatile int *>(bar_load + 21);
+  const uint32_t base = smem_u32(sm), abort = base + M::ABORT;
 
   if (warp == 0) {
-    tmem_alloc(tmem_slot, TMEM_COLS);
+    tmem_alloc(reinterpret_cast<uint32_t *>(sm + M::SLOT), TMEM_COLS);
     tmem_relinquish();
   }
   if (tid == 32) {
-    for (int i = 0; i < NST; ++i) {
-      mbar_init(bar_load + i, 1);
-      mbar_init(bar_free + i, 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar_ready + i, NPREP);
-      mbar_init(bar_kv + i, 1);
-      mbar_init(bar_o + i, 1);
-      mbar_init(bar_oread + i, NFINISH);
-    }
-    mbar_init(bar_p, 1);
-    mbar_init(bar_ds, NFINISH);
-    mbar_init(bar_s, NFINISH);
-    mbar_init(bar_drain, 1);
-    *abort = 0;
+    auto init = [&](uint32_t at, int n, uint32_t count) {
+      for (int i = 0; i < n; ++i) mbar_init(reinterpret_cast<uint64_t *>(sm + at + 8 * i), count);
+    };
+    init(M::LOAD, NST, 1);
+    init(M::FREE, NST, 1);
+    init(M::READY, 2, NPREP);
+    init(M::KV, 2, 1);
+    init(M::OUT, 2, 1);
+    init(M::OREAD, 1, NFINISH);
+    init(M::PF, 1, 1);
+    init(M::PREAD, 1, NPREP);
+    init(M::DS, 1, NFINISH);
+    init(M::SOP, 1, NFINISH);
+    init(M::DRAIN, 1, 1);
+    *reinterpret_cast<uint32_t *>(sm + M::ABORT) = 0;
     fence_mbar_init();
   }
   if (tid >= 64 && tid < 64 + 65) {
@@ -252,17 +299,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = *reinterpret_cast<uint32_t *>(sm + M::SLOT);   // 0: the CTA holds all of tensor memory (the MMA warp writes it so)
   griddep_launch_dependents();
 
   const int beg = it.g * p.seg, end = min(it.len, beg + p.seg);
   const int nch = (end - beg + C - 1) / C;
   const int page = lin_page(p, it.n);
-  float *const final_page = !PHASE1 && last && r.s_final && page >= 0
+  // (the chain kernel has written the end state of a sequence with several segments)
+  float *const final_page = !PHASE1 && it.nseg == 1 && r.s_final && page >= 0
                                 ? r.s_final + (static_cast<size_t>(page) * p.H + h) * DA * DC : nullptr;
   // a state that leaves in fp32 takes all three terms; one that only makes bf16 outputs, two
   const bool three = PHASE1 || final_page;
-  auto chunk_row = [&](int i) { return beg + C * (rev ? nch - 1 - i : i); };
+  const int tail_i = rev ? 0 : nch - 1, tail_n = end - beg - C * (nch - 1);   // the only chunk that may be short
 
   if (warp == NFINISH + NPREP + 1) {
     // ---------------------------------------------------------------- copies
@@ -270,19 +318,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const CUtensorMap *ma = &maps.m[r.ia], *mb = &maps.m[r.ib], *mc = &maps.m[r.ic];
       const int ha = h / p.t[r.ia].div, hb = h / p.t[r.ib].div, hc = h / p.t[r.ic].div;
       constexpr uint32_t bytes = (PHASE1 ? 0 : DA * 128) + DA * 128 + DC * 128;
-      int i = 0;
-      for (; i < nch; ++i) {
-        const int st = i % NST, row = it.t0 + chunk_row(i);
-        uint8_t *dst = sm + M::STAGE * st;
-        if (i >= NST && !wait_or_abort(bar_free + st, (i / NST - 1) & 1, abort)) break;
-        mbar_expect_tx(bar_load + st, bytes);
+      const int step = rev ? -C : C;
+      int row = it.t0 + beg + (rev ? C * (nch - 1) : 0), i = 0;
+      Ring<NST> st;
+      for (; i < nch; ++i, st.next(), row += step) {
+        const uint32_t bar = base + M::LOAD + 8 * st.at, dst = base + M::STAGE * st.at;
+        if (i >= NST && !wait_at(base + M::FREE + 8 * st.at, st.phase ^ 1, abort)) break;
+        expect_at(bar, bytes);
         for (int d = 0; d < DA / 64; ++d) {
-          tma_load_4d(dst + M::B + 8192 * d, mb, bar_load + st, 64 * d, hb, row, it.b);
-          if (!PHASE1) tma_load_4d(dst + M::A + 8192 * d, ma, bar_load + st, 64 * d, ha, row, it.b);
+          load_box(dst + M::B + 8192 * d, mb, bar, 64 * d, hb, row, it.b);
+          if (!PHASE1) load_box(dst + M::A + 8192 * d, ma, bar, 64 * d, ha, row, it.b);
         }
-        for (int d = 0; d < DC / 64; ++d) tma_load_4d(dst + M::CT + 8192 * d, mc, bar_load + st, 64 * d, hc, row, it.b);
+        for (int d = 0; d < DC / 64; ++d) load_box(dst + M::CT + 8192 * d, mc, bar, 64 * d, hc, row, it.b);
         if (i + NST < nch) {   // and the chunk that comes into this stage next, as far as L2
-          const int ahead = it.t0 + chunk_row(i + NST);
+          const int ahead = row + NST * step;
           for (int d = 0; d < DA / 64; ++d) {
             tma_prefetch_4d(mb, 64 * d, hb, ahead, it.b);
             if (!PHASE1) tma_prefetch_4d(ma, 64 * d, ha, ahead, it.b);
@@ -291,73 +340,89 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
       }
       // nothing may land in shared memory after the CTA (each wait bounded)
-      for (int j = i > NST ? i - NST : 0; j < i; ++j) mbar_wait(bar_load + j % NST, (j / NST) & 1);
+      for (int j = i > NST ? i - NST : 0; j < i; ++j)
+        mbar_wait(reinterpret_cast<uint64_t *>(sm + M::LOAD) + j % NST, (j / NST) & 1);
     }
   } else if (warp == NFINISH + NPREP) {
     // ---------------------------------------------------------------- MMAs
-    if (lane == 0) {
-      const uint32_t base = smem_u32(sm);
-      bool ok = true;
-      auto issue_p = [&](int i) -> bool {   // P = a b^T once both landed
-        if (!wait_or_abort(bar_load + i % NST, (i / NST) & 1, abort)) return false;
-        const uint32_t sb = base + M::STAGE * (i % NST);
-        mma_ss_steps<DA / 16, false, true, true>(tmem + COL_P, desc_lo(sb + M::A, 16), 32, desc_lo(sb + M::B, 16), 32,
-                                                 idesc_bf16(C, C, false, false));
-        mma_commit(bar_p);
-        return true;
-      };
-      if (!PHASE1 && nch > 0) ok = issue_p(0);
-      for (int i = 0; ok && i < nch; ++i) {
-        const int st = i % NST, bf = i & 1;
-        const uint32_t bph = (i >> 1) & 1, sb = base + M::STAGE * st;
-        const uint32_t clo = desc_lo(sb + M::CT, 8192);
-        // dS^T = c^T (w b)
-        if (!(ok = wait_or_abort(bar_load + st, (i / NST) & 1, abort) && wait_or_abort(bar_ready + bf, bph, abort))) break;
-        if (i > 0 && !(ok = wait_or_abort(bar_ds, (i - 1) & 1, abort))) break;
-        tc_fence_after();
-        constexpr uint32_t id_kv = idesc_bf16(128, DA, true, true);
-        mma_ss_steps<C / 16, false, false, false>(tmem + COL_DS, clo, 2048, desc_lo(sb + M::B, 8192), 2048, id_kv);
-        mma_ss_steps<C / 16, true, false, false>(tmem + COL_DS, clo, 2048, desc_lo(base + M::M + TILE * bf, 8192), 2048,
-                                                 id_kv);
-        if (three)
-          mma_ss_steps<C / 16, true, false, false>(tmem + COL_DS, clo, 2048,
-                                                   desc_lo(base + M::L + TILE * (i % M::NL), 8192), 2048, id_kv);
-        mma_commit(bar_kv + bf);
-        if (PHASE1) {
-          mma_commit(bar_free + st);
-          continue;
-        }
-        // the next chunk's P (this one's has been read)
-        if (i + 1 < nch && !(ok = issue_p(i + 1))) break;
-        // O1^T = S^T a^T, O2^T = c^T P^T
-        if (!(ok = wait_or_abort(bar_s, i & 1, abort))) break;
-        if (i >= 2 && !(ok = wait_or_abort(bar_oread + bf, ((i - 2) >> 1) & 1, abort))) break;
-        tc_fence_after();
-        const uint32_t co = tmem + COL_O + 128 * bf, alo = desc_lo(sb + M::A, 16);
+    const uint32_t e = elect_one();
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t phase) {
+      ok = ok && warp_wait_at(base + bar, phase, abort);
+      return ok;
+    };
+    Ring<NST> pst;   // of the chunk whose P is formed next
+    auto issue_p = [&]() -> bool {   // P = a b^T once both landed
+      if (!wait(M::LOAD + 8 * pst.at, pst.phase)) return false;
+      tc_fence_after();
+      const uint32_t sb = base + M::STAGE * pst.at, alo = desc_lo(sb + M::A, 16), blo = desc_lo(sb + M::B, 16);
 #pragma unroll
-        for (int kk = 0; kk < DA / 16; ++kk) {
-          const uint32_t a = alo + (kk >> 2) * 512 + (kk & 3) * 2;
-          if (kk == 0) mma_ts_lo<false>(co, tmem + COL_S, a, idesc_bf16(128, C, false, false));
-          else mma_ts_lo<true>(co, tmem + COL_S + 8 * kk, a, idesc_bf16(128, C, false, false));
-        }
-        mma_ss_steps<C / 16, false, false, false>(co + 64, clo, 2048, desc_lo(base + M::P + 8192 * bf, 16), 32,
-                                                  idesc_bf16(128, C, true, false));
-        mma_commit(bar_o + bf);
-        mma_commit(bar_free + st);
+      for (int kk = 0; kk < DA / 16; ++kk) {
+        const uint32_t o = (kk >> 2) * 512 + (kk & 3) * 2;
+        if (kk == 0) mma_ss_lo<false>(T::P, alo, blo, idesc_bf16(C, C, false, false), e);
+        else mma_ss_lo<true>(T::P, alo + o, blo + o, idesc_bf16(C, C, false, false), e);
       }
-      if (!ok) {   // a wait gave up: the MMAs in flight finish before the memory they use is released
-        mma_commit(bar_drain);
-        mbar_wait(bar_drain, 0);
+      commit_one(base + M::PF, e);
+      pst.next();
+      return true;
+    };
+    if (!PHASE1 && nch > 0) issue_p();
+    Ring<NST> st;
+    Ring<2> bf;
+    for (int i = 0; ok && i < nch; ++i, st.next(), bf.next()) {
+      const uint32_t sb = base + M::STAGE * st.at, one = i & 1;
+      // the next chunk's P, as soon as this one's is read
+      if (!PHASE1 && i + 1 < nch && (!wait(M::PREAD, one) || !issue_p())) break;
+      // dS^T = (w c)^T b
+      if (PHASE1 && !wait(M::LOAD + 8 * st.at, st.phase)) break;
+      if (!wait(M::READY + 8 * bf.at, bf.phase)) break;
+      if (i > 0 && !wait(M::DS, one ^ 1)) break;
+      tc_fence_after();
+      const uint32_t blo = desc_lo(sb + M::B, 8192), wcol = T::term(PHASE1 || !three ? bf.at : 0, 0);
+#pragma unroll
+      for (int t = 0; t < 3; ++t)
+        if (t < 2 || three)
+#pragma unroll
+          for (int kk = 0; kk < C / 16; ++kk) {
+            if (t + kk == 0) mma_ts_lo<false>(T::DS, wcol, blo, idesc_bf16(128, DA, false, true), e);
+            else mma_ts_lo<true>(T::DS, wcol + 32 * t + 8 * kk, blo + 128 * kk, idesc_bf16(128, DA, false, true), e);
+          }
+      commit_one(base + M::KV + 8 * bf.at, e);
+      if (PHASE1) {
+        commit_one(base + M::FREE + 8 * st.at, e);
+        continue;
       }
+      // O1^T = S^T a^T, O2^T = c^T P^T
+      if (!wait(M::SOP, one)) break;
+      if (i > 0 && !wait(M::OREAD, one ^ 1)) break;
+      tc_fence_after();
+      const uint32_t alo = desc_lo(sb + M::A, 16), clo = desc_lo(sb + M::CT, 8192), plo = desc_lo(base + M::P + 8192 * bf.at, 16);
+#pragma unroll
+      for (int kk = 0; kk < DA / 16; ++kk) {
+        const uint32_t a = alo + (kk >> 2) * 512 + (kk & 3) * 2;
+        if (kk == 0) mma_ts_lo<false>(T::O, T::S, a, idesc_bf16(128, C, false, false), e);
+        else mma_ts_lo<true>(T::O, T::S + 8 * kk, a, idesc_bf16(128, C, false, false), e);
+      }
+#pragma unroll
+      for (int kk = 0; kk < C / 16; ++kk) {
+        if (kk == 0) mma_ss_lo<false>(T::O + 64, clo, plo, idesc_bf16(128, C, true, false), e);
+        else mma_ss_lo<true>(T::O + 64, clo + 128 * kk, plo + 2 * kk, idesc_bf16(128, C, true, false), e);
+      }
+      commit_one(base + M::OUT + 8 * bf.at, e);
+      commit_one(base + M::FREE + 8 * st.at, e);
+    }
+    if (!ok) {   // a wait gave up: the MMAs in flight finish before the memory they use is released
+      commit_one(base + M::DRAIN, e);
+      mbar_wait(reinterpret_cast<uint64_t *>(sm + M::DRAIN), 0);
     }
   } else if (warp >= NFINISH) {
-    // ---------------------------------------------------------------- prep: P and w b
+    // ---------------------------------------------------------------- prep: P and w c
     const int quad = warp & 3, half = (warp - NFINISH) >> 2;
-    const int row = tid & 63, piece = (tid >> 6) & 3;   // w b: four threads per row
     const float bscale = r.bscale;
     const uint32_t lrow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    // P: rows t = 16 quad + lane / 4 (+ 8), columns s = 32 half + 8 j + 2 (lane % 4) (+ 1); the decays
-    // are the same for every chunk
+    const bool has_c = 32 * quad < DC;
+    const int s0 = 32 * half + 2 * (lane & 3);   // this thread's tokens: s0 + 8 j (+ 1), j = 0 .. 3
+    // P: rows t = 16 quad + lane / 4 (+ 8), columns s0 + 8 j (+ 1); the decays are the same for every chunk
     uint64_t dec[4][2];
     if (!PHASE1) {
       const float f = bscale * r.yscale;
@@ -365,28 +430,73 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int t = 16 * quad + (lane >> 2) + 8 * k, s = 32 * half + 8 * j + 2 * (lane & 3);
+          const int t = 16 * quad + (lane >> 2) + 8 * k, s = s0 + 8 * j;
           const int d = rev ? s - t : t - s, d1 = rev ? d + 1 : d - 1;
           dec[j][k] = pair_f32(d >= 0 ? f * pw[max(d, 0)] : 0.f, d1 >= 0 ? f * pw[max(d1, 0)] : 0.f);
         }
     }
+    // stmatrix of P: matrix m = rows 8 (m & 1) .., columns 8 (m / 2) ..
+    const int tp = 16 * quad + (lane & 15), cp = 4 * half + (lane >> 4);
+    const uint32_t put0 = base + M::P + sw128(tp, cp), put1 = base + M::P + sw128(tp, cp + 2);
+    // w c: lanes dc = 32 quad + 16 g + lane / 4 (+ 8), tokens s0 + 8 j (+ 1)
+    uint64_t wgt[4];
+    auto weights = [&](int n) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int s = s0 + 8 * j;
+        wgt[j] = pair_f32(bscale * pw[rev ? s + 1 : max(n - 1 - s, 0)], bscale * pw[rev ? s + 2 : max(n - 2 - s, 0)]);
+      }
+    };
+    weights(C);
+    // ldmatrix of c: matrix m = tokens 8 (j + m / 2) .., columns 8 (m & 1) ..; its row q = token
+    const int sq = 32 * half + 8 * (lane >> 4) + (lane & 7), dq = 32 * quad + 8 * ((lane >> 3) & 1);
+    const uint32_t get0 = base + M::CT + (dq >> 6) * 8192 + sw128(sq, (dq & 63) >> 3);
+    const uint32_t get1 = base + M::CT + ((dq + 16) >> 6) * 8192 + sw128(sq, ((dq + 16) & 63) >> 3);
     const uint64_t minus_one = pair_f32(-1.f, -1.f);
-    for (int i = 0; i < nch; ++i) {
-      const int st = i % NST, bf = i & 1;
-      uint8_t *sb = sm + M::STAGE * st, *mid_t = sm + M::M + TILE * bf, *lo_t = sm + M::L + TILE * (i % M::NL);
-      const int n = min(C, end - chunk_row(i));
-      if (!__all_sync(0xffffffffu, wait_or_abort(bar_load + st, (i / NST) & 1, abort))) break;
-      // this chunk's buffers are those of the products of two chunks ago (a single third-term buffer: of
-      // the last one), which P's and b's arrival do not imply
-      if (i >= 2 && !__all_sync(0xffffffffu, wait_or_abort((PHASE1 ? bar_kv : bar_o) + bf, ((i - 2) >> 1) & 1, abort))) break;
-      if (M::NL == 1 && three && i >= 1 &&
-          !__all_sync(0xffffffffu, wait_or_abort(bar_kv + (bf ^ 1), ((i - 1) >> 1) & 1, abort))) break;
+    auto weigh = [&](uint32_t stage, uint32_t col, int n, auto terms) {
+      constexpr int TERMS = decltype(terms)::value;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t v[8], t1[8], t2[8];
+#pragma unroll
+        for (int j = 0; j < 4; j += 2)
+          ldmatrix4_trans((g ? get1 : get0) + stage + 1024 * j, v[2 * j], v[2 * j + 1], v[2 * j + 2], v[2 * j + 3]);
+        if (n < C)   // tokens behind the sequence's end count for nothing, whatever they hold
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int s = s0 + 8 * (j >> 1);
+            v[j] &= s + 1 < n ? 0xffffffffu : s < n ? 0xffffu : 0u;
+          }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) split_pair<TERMS>(v[j], wgt[j >> 1], minus_one, v[j], t1[j], t2[j]);
+        const uint32_t at = col + (static_cast<uint32_t>(16 * g) << 16);
+        tmem_st_frag4(at, v);
+        tmem_st_frag4(at + 32, t1);
+        if (TERMS == 3) tmem_st_frag4(at + 64, t2);
+      }
+    };
+    const uint32_t wlane = lrow + 16 * half;
+    if (!has_c) {   // value widths of 64: the upper lanes' operand is zero
+      const uint32_t zero[8] = {};
+      for (int t = 0; t < (PHASE1 ? 8 : 4); ++t)   // every column of the buffers
+        for (int g = 0; g < 2; ++g) tmem_st_frag4(wlane + (static_cast<uint32_t>(16 * g) << 16) + T::term(0, t), zero);
+    }
+    Ring<NST> st;
+    Ring<2> bf;
+    for (int i = 0; i < nch; ++i, st.next(), bf.next()) {
+      const int n = i == tail_i ? tail_n : C;
+      if (!warp_wait_at(base + M::LOAD + 8 * st.at, st.phase, abort)) break;
+      // this chunk's buffers are those of the products of two chunks ago
+      if (i >= 2 && !warp_wait_at(base + (PHASE1 ? M::KV : M::OUT) + 8 * bf.at, bf.phase ^ 1, abort)) break;
       if (!PHASE1) {
-        if (!__all_sync(0xffffffffu, wait_or_abort(bar_p, i & 1, abort))) break;
+        if (!warp_wait_at(base + M::PF, i & 1, abort)) break;
         tc_fence_after();
         float v[16];
-        tmem_ld_frag4(lrow + COL_P + 32 * half, v);
+        tmem_ld_frag4(lrow + T::P + 32 * half, v);
         tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_at(base + M::PREAD);
         uint32_t u[4][2];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -394,53 +504,45 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           for (int k = 0; k < 2; ++k) {
             float y0, y1;
             unpair_f32(mul_f32x2(pair_f32(v[4 * j + 2 * k], v[4 * j + 2 * k + 1]), dec[j][k]), y0, y1);
-            if (n < C) {   // whatever lies behind the sequence's end has no part in this
-              const int s = 32 * half + 8 * j + 2 * (lane & 3);
-              y0 = s < n ? y0 : 0.f;
-              y1 = s + 1 < n ? y1 : 0.f;
-            }
             u[j][k] = pack_bf16x2(y0, y1);
           }
-        const int t = 16 * quad + (lane & 15), ch = 4 * half + (lane >> 4);
-        stmatrix4(smem_u32(sm + M::P + 8192 * bf + sw128(t, ch)), u[0][0], u[0][1], u[1][0], u[1][1]);
-        stmatrix4(smem_u32(sm + M::P + 8192 * bf + sw128(t, ch + 2)), u[2][0], u[2][1], u[3][0], u[3][1]);
+        if (n < C)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t keep = s0 + 8 * j + 1 < n ? 0xffffffffu : s0 + 8 * j < n ? 0xffffu : 0u;
+            u[j][0] &= keep;
+            u[j][1] &= keep;
+          }
+        stmatrix4(put0 + 8192 * bf.at, u[0][0], u[0][1], u[1][0], u[1][1]);
+        stmatrix4(put1 + 8192 * bf.at, u[2][0], u[2][1], u[3][0], u[3][1]);
+        // one buffer of three terms: the last chunk's product has to be complete
+        if (three && i >= 1 && !warp_wait_at(base + M::KV + 8 * (bf.at ^ 1), bf.phase ^ (bf.at ^ 1), abort)) break;
       }
-      if (row < n) {
-        const float w = pw[rev ? row + 1 : n - 1 - row] * bscale;
-        const uint64_t w2 = pair_f32(w, w);
-#pragma unroll
-        for (int jj = 0; jj < DA / 32; ++jj) {
-          const int j = piece * (DA / 32) + jj;
-          const uint32_t off = (j >> 3) * 8192 + sw128(row, j & 7);
-          uint4 v = *reinterpret_cast<const uint4 *>(sb + M::B + off), mid, lo;
-          split_pair(v.x, w2, minus_one, three, v.x, mid.x, lo.x);
-          split_pair(v.y, w2, minus_one, three, v.y, mid.y, lo.y);
-          split_pair(v.z, w2, minus_one, three, v.z, mid.z, lo.z);
-          split_pair(v.w, w2, minus_one, three, v.w, mid.w, lo.w);
-          *reinterpret_cast<uint4 *>(sb + M::B + off) = v;
-          *reinterpret_cast<uint4 *>(mid_t + off) = mid;
-          if (three) *reinterpret_cast<uint4 *>(lo_t + off) = lo;
+      tc_fence_after();
+      if (n < C) weights(n);
+      if (has_c) {
+        const uint32_t col = wlane + T::term(PHASE1 || !three ? bf.at : 0, 0);
+        if (three) weigh(M::STAGE * st.at, col, n, std::integral_constant<int, 3>());
+        else weigh(M::STAGE * st.at, col, n, std::integral_constant<int, 2>());
+      }
+      tmem_wait_st();
+      if (n < C) {
+        // rows behind the sequence's end, which the products read as well, become zeros (once all of c is
+        // read; P has been formed, and is cleared of them above)
+        named_bar_sync(1, 32 * NPREP);
+        uint8_t *sb = sm + M::STAGE * st.at;
+        const int row = tid & 63, piece = (tid >> 6) & 3;
+        if (row >= n) {
+          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+          for (int j = piece; j < DA / 8; j += 4) *reinterpret_cast<uint4 *>(sb + M::B + (j >> 3) * 8192 + sw128(row, j & 7)) = zero;
+          for (int j = piece; j < DC / 8; j += 4) *reinterpret_cast<uint4 *>(sb + M::CT + (j >> 3) * 8192 + sw128(row, j & 7)) = zero;
         }
-      } else {   // rows behind the sequence's end: zeros, in c too
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int jj = 0; jj < DA / 32; ++jj) {
-          const int j = piece * (DA / 32) + jj;
-          const uint32_t off = (j >> 3) * 8192 + sw128(row, j & 7);
-          *reinterpret_cast<uint4 *>(sb + M::B + off) = zero;
-          *reinterpret_cast<uint4 *>(mid_t + off) = zero;
-          *reinterpret_cast<uint4 *>(lo_t + off) = zero;
-        }
-#pragma unroll
-        for (int jj = 0; jj < DC / 32; ++jj) {
-          const int j = piece * (DC / 32) + jj;
-          *reinterpret_cast<uint4 *>(sb + M::CT + (j >> 3) * 8192 + sw128(row, j & 7)) = zero;
-        }
+        weights(C);
       }
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_ready + bf);
+      if (lane == 0) arrive_at(base + M::READY + 8 * bf.at);
     }
   } else {
     // ---------------------------------------------------------------- finish: the state and the outputs
@@ -486,12 +588,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         unpair_f32(S[m], a, b);
         u[m] = pack_bf16x2(a, b);
       }
-      if constexpr (SN == 32) tmem_st16(lrow + COL_S + part * 16, u);
-      else tmem_st8(lrow + COL_S + part * 8, u);
+      if constexpr (SN == 32) tmem_st16(lrow + T::S + part * 16, u);
+      else tmem_st8(lrow + T::S + part * 8, u);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_s);
+      if (lane == 0) arrive_at(base + M::SOP);
     };
     if (!PHASE1) store_operand();
     // the output: this warp's 32 columns dc and 16 tokens t, through its 1 KB of shared
@@ -501,7 +603,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const float yscale = r.yscale;
     const size_t ystep = static_cast<size_t>(p.H) * DC;
     const int tf = 16 * part + 2 * (lane & 3), tr = 16 * part + (lane >> 2);
-    const uint32_t stage = smem_u32(sm + M::Y + 1024 * warp);
+    const uint32_t stage = base + M::Y + 1024 * warp;
     // stmatrix: matrix m = tokens 8 (m / 2) .., columns 8 (m & 1) ..; its row q = token
     const int tq = 8 * (lane >> 4) + (lane & 7), cq = (lane >> 3) & 1;
     const uint32_t put0 = stage + tq * 64 + (((cq ^ (tq >> 1)) & 3) << 4), put1 = stage + tq * 64 + ((((2 + cq) ^ (tq >> 1)) & 3) << 4);
@@ -518,18 +620,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
     };
     if (has_y && nch > 0) {
-      const size_t row = static_cast<size_t>(it.b) * p.T + it.t0 + chunk_row(0);
+      const size_t row = static_cast<size_t>(it.b) * p.T + it.t0 + beg + (rev ? C * (nch - 1) : 0);
       if (y_f32) yrow = reinterpret_cast<uint8_t *>(static_cast<float *>(r.y) + (row + tf) * ystep + h * DC + 32 * quad + (lane >> 2));
       else yrow = reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(r.y) + (row + tr) * ystep + h * DC + 32 * quad + 8 * (lane & 3));
       gamma(C, gam);
     }
     bool ok = true;
-    for (int i = 0; i < nch; ++i) {
-      const int bf = i & 1;
-      const uint32_t bph = (i >> 1) & 1;
-      const int n = min(C, end - chunk_row(i));
+    Ring<2> bf;
+    for (int i = 0; i < nch; ++i, bf.next()) {
+      const int n = i == tail_i ? tail_n : C;
       // S <- lambda^n S + dS
-      if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar_kv + bf, bph, abort)))) break;
+      if (!(ok = warp_wait_at(base + M::KV + 8 * bf.at, bf.phase, abort))) break;
       tc_fence_after();
       {
         const float g = n == C ? decay.next() : pw[n];
@@ -537,7 +638,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
         for (int q = 0; q < SN / 16; ++q) {
           float v[16];
-          tmem_ld16(lrow + COL_DS + da0 + 16 * q, v);
+          tmem_ld16(lrow + T::DS + da0 + 16 * q, v);
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 8; ++e) S[8 * q + e] = fma_f32x2(g2, S[8 * q + e], pair_f32(v[2 * e], v[2 * e + 1]));
@@ -545,19 +646,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_ds);
+      if (lane == 0) arrive_at(base + M::DS);
       if (PHASE1) continue;
 
       // its operand for the next chunk, once O1^T has been formed from this one's
-      if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar_o + bf, bph, abort)))) break;
+      if (!(ok = warp_wait_at(base + M::OUT + 8 * bf.at, bf.phase, abort))) break;
       tc_fence_after();
       if (i + 1 < nch) store_operand();
       if (!has_y) {
-        if (lane == 0) mbar_arrive(bar_oread + bf);
+        if (lane == 0) arrive_at(base + M::OREAD);
         continue;
       }
       if (n < C) gamma(n, gam);
-      const uint32_t col = lrow + COL_O + 128 * bf + 16 * part;
+      const uint32_t col = lrow + T::O + 16 * part;
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {   // 16 lanes of tensor memory: dc = 32 quad + 16 hh ..
         float v1[8], v2[8];
@@ -568,7 +669,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (hh == 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_oread + bf);
+          if (lane == 0) arrive_at(base + M::OREAD);
         }
         uint64_t y[2][2];
 #pragma unroll
@@ -631,7 +732,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && *abort) atomicOr(&g_gdr_linear_error, 1);
+  if (tid == 0 && *reinterpret_cast<volatile uint32_t *>(sm + M::ABORT)) atomicOr(&g_gdr_linear_error, 1);
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);

@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(kWarps * 32) linear_token_kernel(const LinProb
   const LinItem it = lin_item(p, x);
   if (!it.ok) return;
   const bool last = r.reverse ? it.g == 0 : it.g == it.nseg - 1;    // in the run's order
-  if (PHASE1 && last) return;
+  if (PHASE1 && last && (it.nseg == 1 || !r.s_final)) return;
   const int c0 = cg * 8, dc = r.dc;
   const float ld = __ldg(p.log_decay + h);
   // lambda as a sum of two fp32 values: its own rounding, compounded over a memory of
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kWarps * 32) linear_token_kernel(const LinProb
 
   float *dst = nullptr;
   if (PHASE1) dst = r.X + (static_cast<size_t>(x) * p.H + h) * DA * dc;
-  else if (last && r.s_final && page >= 0) dst = r.s_final + (static_cast<size_t>(page) * p.H + h) * DA * dc;
+  else if (it.nseg == 1 && r.s_final && page >= 0) dst = r.s_final + (static_cast<size_t>(page) * p.H + h) * DA * dc;
   if (dst) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {

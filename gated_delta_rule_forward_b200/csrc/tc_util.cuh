@@ -215,6 +215,24 @@ __device__ __forceinline__ void stmatrix4_trans(uint32_t saddr, uint32_t r0, uin
                : "memory");
 }
 
+// 16 lanes x 16 columns of 32 bits from registers in the layout of 8x8 matrices of 16-bit
+// pairs: r[2 j], r[2 j + 1] are rows lane / 4 and lane / 4 + 8, column 4 j + lane % 4.
+__device__ __forceinline__ void tmem_st_frag4(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// Four 8x8 matrices of 16-bit values from shared memory, each transposed: lane 8 m + q gives
+// the address of row q of matrix m, and register m receives column lane / 4, rows
+// 2 (lane % 4) + {0, 1} of it.
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t saddr, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(saddr)
+               : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ---------------------------------------------------------------- UMMA
