@@ -221,22 +221,17 @@ struct ChunkDecay {
 // w x of two bf16 values x as a sum of bf16 pairs: two terms keep 16 significant bits,
 // three keep 24.
 template <int TERMS>
-__device__ __forceinline__ void split_pair(uint32_t x, uint64_t w, uint64_t minus_one, uint32_t &hi, uint32_t &mid,
-                                           uint32_t &lo) {
-  const uint64_t p = mul_f32x2(pair_f32(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), w);
-  float a, b;
-  unpair_f32(p, a, b);
+__device__ __forceinline__ void split_pair(uint32_t x, float w0, float w1, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+  const float a = __uint_as_float(x << 16) * w0, b = __uint_as_float(x & 0xffff0000u) * w1;
   hi = pack_bf16x2(a, b);
-  const uint64_t r = fma_f32x2(pair_f32(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)), minus_one, p);
-  unpair_f32(r, a, b);
-  mid = pack_bf16x2(a, b);
-  if (TERMS == 3) {
-    unpair_f32(fma_f32x2(pair_f32(__uint_as_float(mid << 16), __uint_as_float(mid & 0xffff0000u)), minus_one, r), a, b);
-    lo = pack_bf16x2(a, b);
-  }
+  const float ra = a - __uint_as_float(hi << 16), rb = b - __uint_as_float(hi & 0xffff0000u);
+  mid = pack_bf16x2(ra, rb);
+  if (TERMS == 3)
+    lo = pack_bf16x2(ra - __uint_as_float(mid << 16), rb - __uint_as_float(mid & 0xffff0000u));
 }
 
-template <int DA, int DC, bool PHASE1>
+// YF32: y in fp32 (the value heads' shares of a shared head's gradient).
+template <int DA, int DC, bool PHASE1, bool YF32>
 __global__ void __launch_bounds__(NTHREADS, 1)
     linear_chunk_kernel(const __grid_constant__ LinProblem p, const __grid_constant__ LinChunkMaps maps,
                         const LinRunSel sel) {
@@ -439,12 +434,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int tp = 16 * quad + (lane & 15), cp = 4 * half + (lane >> 4);
     const uint32_t put0 = base + M::P + sw128(tp, cp), put1 = base + M::P + sw128(tp, cp + 2);
     // w c: lanes dc = 32 quad + 16 g + lane / 4 (+ 8), tokens s0 + 8 j (+ 1)
-    uint64_t wgt[4];
+    float wgt[4][2];
     auto weights = [&](int n) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int s = s0 + 8 * j;
-        wgt[j] = pair_f32(bscale * pw[rev ? s + 1 : max(n - 1 - s, 0)], bscale * pw[rev ? s + 2 : max(n - 2 - s, 0)]);
+        wgt[j][0] = bscale * pw[rev ? s + 1 : max(n - 1 - s, 0)];
+        wgt[j][1] = bscale * pw[rev ? s + 2 : max(n - 2 - s, 0)];
       }
     };
     weights(C);
@@ -452,7 +448,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int sq = 32 * half + 8 * (lane >> 4) + (lane & 7), dq = 32 * quad + 8 * ((lane >> 3) & 1);
     const uint32_t get0 = base + M::CT + (dq >> 6) * 8192 + sw128(sq, (dq & 63) >> 3);
     const uint32_t get1 = base + M::CT + ((dq + 16) >> 6) * 8192 + sw128(sq, ((dq + 16) & 63) >> 3);
-    const uint64_t minus_one = pair_f32(-1.f, -1.f);
     auto weigh = [&](uint32_t stage, uint32_t col, int n, auto terms) {
       constexpr int TERMS = decltype(terms)::value;
 #pragma unroll
@@ -468,7 +463,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             v[j] &= s + 1 < n ? 0xffffffffu : s < n ? 0xffffu : 0u;
           }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) split_pair<TERMS>(v[j], wgt[j >> 1], minus_one, v[j], t1[j], t2[j]);
+        for (int j = 0; j < 8; ++j) split_pair<TERMS>(v[j], wgt[j >> 1][0], wgt[j >> 1][1], v[j], t1[j], t2[j]);
         const uint32_t at = col + (static_cast<uint32_t>(16 * g) << 16);
         tmem_st_frag4(at, v);
         tmem_st_frag4(at + 32, t1);
@@ -599,7 +594,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // the output: this warp's 32 columns dc and 16 tokens t, through its 1 KB of shared
     // memory (rows t of 64 bytes, 16-byte chunks XOR-ed with t / 2) unless in fp32.
     // Fragment tiles: lane holds dc = 16 hh + lane / 4 (+ 8), t = 8 j + 2 (lane % 4) (+ 1).
-    const bool has_y = !PHASE1 && quad * 32 < DC, y_f32 = r.y_f32 != 0;
+    const bool has_y = !PHASE1 && quad * 32 < DC;
     const float yscale = r.yscale;
     const size_t ystep = static_cast<size_t>(p.H) * DC;
     const int tf = 16 * part + 2 * (lane & 3), tr = 16 * part + (lane >> 2);
@@ -610,7 +605,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t get = stage + (lane >> 2) * 64 + ((((lane & 3) ^ (lane >> 3)) & 3) << 4);   // and 512 bytes on: token + 8
     // row tr's address in this chunk, advanced chunk by chunk; full chunks' decays
     uint8_t *yrow = nullptr;
-    const long long yadvance = (rev ? -C : C) * static_cast<long long>(ystep) * (y_f32 ? 4 : 2);
+    const long long yadvance = (rev ? -C : C) * static_cast<long long>(ystep) * (YF32 ? 4 : 2);
     uint64_t gam[2] = {0, 0};
     auto gamma = [&](int n, uint64_t (&g)[2]) {
 #pragma unroll
@@ -621,7 +616,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     };
     if (has_y && nch > 0) {
       const size_t row = static_cast<size_t>(it.b) * p.T + it.t0 + beg + (rev ? C * (nch - 1) : 0);
-      if (y_f32) yrow = reinterpret_cast<uint8_t *>(static_cast<float *>(r.y) + (row + tf) * ystep + h * DC + 32 * quad + (lane >> 2));
+      if (YF32) yrow = reinterpret_cast<uint8_t *>(static_cast<float *>(r.y) + (row + tf) * ystep + h * DC + 32 * quad + (lane >> 2));
       else yrow = reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(r.y) + (row + tr) * ystep + h * DC + 32 * quad + 8 * (lane & 3));
       gamma(C, gam);
     }
@@ -679,7 +674,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             y[j][k] = fma_f32x2(gam[j], pair_f32(v1[4 * j + 2 * k], v1[4 * j + 2 * k + 1]),
                                 pair_f32(v2[4 * j + 2 * k], v2[4 * j + 2 * k + 1]));
         float a, b;
-        if (y_f32) {
+        if constexpr (YF32) {
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -701,7 +696,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           stmatrix4_trans(hh ? put1 : put0, u[0][0], u[0][1], u[1][0], u[1][1]);
         }
       }
-      if (!y_f32) {
+      if constexpr (!YF32) {
         __syncwarp();
         uint4 v0, v1;
         ld_shared_v4(get, v0);
@@ -739,10 +734,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
 }
 
-template <int DA, int DC, bool PHASE1>
+template <int DA, int DC, bool PHASE1, bool YF32>
 cudaError_t launch(const LinProblem &p, const LinChunkMaps &maps, const LinRunSel &sel, bool pdl, cudaStream_t s) {
   constexpr uint32_t SMEM = Smem<PHASE1>::BYTES;
-  auto kern = linear_chunk_kernel<DA, DC, PHASE1>;
+  auto kern = linear_chunk_kernel<DA, DC, PHASE1, YF32>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -758,13 +753,13 @@ cudaError_t launch(const LinProblem &p, const LinChunkMaps &maps, const LinRunSe
   return cudaLaunchKernelEx(&cfg, kern, p, maps, sel);
 }
 
-template <bool PHASE1>
+template <bool PHASE1, bool YF32>
 cudaError_t launch_shape(int da, int dc, const LinProblem &p, const LinChunkMaps &m, const LinRunSel &sel, bool pdl,
                          cudaStream_t s) {
-  if (da == 128 && dc == 128) return launch<128, 128, PHASE1>(p, m, sel, pdl, s);
-  if (da == 128 && dc == 64) return launch<128, 64, PHASE1>(p, m, sel, pdl, s);
-  if (da == 64 && dc == 128) return launch<64, 128, PHASE1>(p, m, sel, pdl, s);
-  return launch<64, 64, PHASE1>(p, m, sel, pdl, s);
+  if (da == 128 && dc == 128) return launch<128, 128, PHASE1, YF32>(p, m, sel, pdl, s);
+  if (da == 128 && dc == 64) return launch<128, 64, PHASE1, YF32>(p, m, sel, pdl, s);
+  if (da == 64 && dc == 128) return launch<64, 128, PHASE1, YF32>(p, m, sel, pdl, s);
+  return launch<64, 64, PHASE1, YF32>(p, m, sel, pdl, s);
 }
 
 }  // namespace
@@ -802,19 +797,23 @@ bool gdr_linear_chunk_maps(const gdr::LinProblem &p, gdr::LinChunkMaps *maps) {
 
 cudaError_t gdr_launch_linear_chunk(const gdr::LinProblem &p, const gdr::LinChunkMaps &maps, bool phase1, bool pdl,
                                     cudaStream_t s) {
-  // one launch for all runs of a shape, so that they read their common tensors at about the same time
+  // one launch for all runs of a shape and output type, so that they read their common tensors at about the same time
   bool done[gdr::kLinMaxRuns] = {};
   for (int i = 0; i < p.nrun; ++i) {
     if (done[i]) continue;
+    const gdr::LinRun &a = p.run[i];
     gdr::LinRunSel sel = {};
-    for (int j = i; j < p.nrun; ++j)
-      if (!done[j] && p.run[j].da == p.run[i].da && p.run[j].dc == p.run[i].dc) {
-        sel.run[sel.n++] = j;
-        done[j] = true;
-      }
+    for (int j = i; j < p.nrun; ++j) {
+      const gdr::LinRun &b = p.run[j];
+      if (done[j] || b.da != a.da || b.dc != a.dc || (!phase1 && b.y_f32 != a.y_f32)) continue;
+      sel.run[sel.n++] = j;
+      done[j] = true;
+    }
     // a programmatic dependent waits for the one launch before it, so only the phase's first one may be it
-    const cudaError_t e = phase1 ? gdr::tc::launch_shape<true>(p.run[i].da, p.run[i].dc, p, maps, sel, pdl && i == 0, s)
-                                 : gdr::tc::launch_shape<false>(p.run[i].da, p.run[i].dc, p, maps, sel, pdl && i == 0, s);
+    const bool dep = pdl && i == 0;
+    const cudaError_t e = phase1    ? gdr::tc::launch_shape<true, false>(a.da, a.dc, p, maps, sel, dep, s)
+                          : a.y_f32 ? gdr::tc::launch_shape<false, true>(a.da, a.dc, p, maps, sel, dep, s)
+                                    : gdr::tc::launch_shape<false, false>(a.da, a.dc, p, maps, sel, dep, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
