@@ -14,7 +14,7 @@
 //     O1^T [dc][t]  = S^T a^T        M128 N64  K = da
 //     O2^T [dc][t]  = c^T P^T        M128 N64  K = 64   (P back through shared memory in bf16)
 // and Y^T = yscale (Gamma_t O1^T + O2^T).  The fp32 state lives in registers of
-// 16 warps: lane dc of a quad, a quarter of da per thread; S <- lambda^n S + dS
+// 8 warps: lane dc of a quad, half of da per thread; S <- lambda^n S + dS
 // is one pass over it.  What bounds the sweep on the chip is the 128 bytes a clock
 // of shared memory: weighting c on its way into tensor memory, rather than b in
 // place, takes 64 KB of a chunk's 272 KB off it.
@@ -31,7 +31,8 @@
 //     copies (1 warp)    a, b, c of the chunks to come, each into the stage of one that is done
 //     prep   (8 warps)   P and w c of chunk i + 1
 //     MMAs   (1 warp)    dS(i), P(i + 1), O1(i), O2(i)
-//     finish (16 warps)  S after chunk i, its bf16 operand, the output rows of chunk i
+//     state  (8 warps)   S after chunk i, its bf16 operand
+//     output (8 warps)   the rows of chunk i
 // Only S -> operand -> O1 is a chain from chunk to chunk.
 #include <type_traits>
 
@@ -48,8 +49,18 @@ namespace tc {
 namespace {
 
 constexpr int C = 64;
-constexpr int NFINISH = 16, NPREP = 8;   // warps 0 .. 15 and 16 .. 23, then the MMA and the copy warp
-constexpr int NTHREADS = 32 * (NFINISH + NPREP + 2);
+// warps 0-7 state, 8-15 output, 16-23 prep, then the MMA and the copy warp (and two idle
+// ones that complete their warpgroup)
+constexpr int NSTATE = 8, NOUT = 8, NPREP = 8;
+constexpr int W_OUT = NSTATE, W_PREP = W_OUT + NOUT, W_MMA = W_PREP + NPREP, W_COPY = W_MMA + 1;
+constexpr int NTHREADS = 32 * (W_MMA + 4);
+// registers a thread: 72 at launch, moved to the threads that hold the state
+constexpr int R_STATE = 112, R_OUT = 64, R_PREP = 64, R_CTL = 24;
+static_assert(32 * (NSTATE * R_STATE + NOUT * R_OUT + NPREP * R_PREP + 4 * R_CTL) <= 72 * NTHREADS, "register split");
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 constexpr uint32_t TILE = 16384;        // 64 rows of two 128-byte atoms
 // Shared memory.  The copies run NST chunks ahead.
 template <bool PHASE1>
@@ -60,8 +71,8 @@ struct Smem {
   static constexpr uint32_t A = 2 * TILE;
   static constexpr uint32_t STAGE = (PHASE1 ? 2 : 3) * TILE;
   static constexpr uint32_t P = NST * STAGE;     // bf16 P, rows t, 8 KB, two buffers
-  static constexpr uint32_t Y = P + (PHASE1 ? 0 : 2 * 8192);      // 1 KB of output rows per finishing warp
-  static constexpr uint32_t PW = Y + (PHASE1 ? 0 : 1024 * NFINISH);   // lambda^0 .. lambda^64, then what fp32 loses of them
+  static constexpr uint32_t Y = P + (PHASE1 ? 0 : 2 * 8192);      // 2 KB of output rows per output warp
+  static constexpr uint32_t PW = Y + (PHASE1 ? 0 : 2048 * NOUT);   // lambda^0 .. lambda^64, then what fp32 loses of them
   static constexpr uint32_t BAR = PW + 2 * 65 * 4 + 8;
   // barriers per stage
   static constexpr uint32_t LOAD = BAR;              // a, b and c landed
@@ -71,11 +82,11 @@ struct Smem {
   static constexpr uint32_t KV = READY + 16;         // dS^T formed
   static constexpr uint32_t OUT = KV + 16;           // O1^T and O2^T formed
   // one each
-  static constexpr uint32_t OREAD = OUT + 16;        // O1^T and O2^T read (16 warps)
+  static constexpr uint32_t OREAD = OUT + 16;        // O1^T and O2^T read (8 warps)
   static constexpr uint32_t PF = OREAD + 8;          // P formed
   static constexpr uint32_t PREAD = PF + 8;          // P read (8 warps)
-  static constexpr uint32_t DS = PREAD + 8;          // dS^T read (16 warps)
-  static constexpr uint32_t SOP = DS + 8;            // S^T of the chunk's start in tensor memory (16 warps)
+  static constexpr uint32_t DS = PREAD + 8;          // dS^T read (8 warps)
+  static constexpr uint32_t SOP = DS + 8;            // S^T of the chunk's start in tensor memory (8 warps)
   static constexpr uint32_t DRAIN = SOP + 8;
   static constexpr uint32_t SLOT = DRAIN + 8;        // tensor-memory address
   static constexpr uint32_t ABORT = SLOT + 4;        // a wait gave up
@@ -109,25 +120,35 @@ __device__ __forceinline__ uint32_t elect_one() {
 }
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
 constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);   // sbo 1024, version 1, SWIZZLE_128B
-template <bool ACC>
-__device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t e) {
+__device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t acc,
+                                          uint32_t e) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
       "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(alo), "r"(blo), "r"(idesc), "n"(ACC ? 1 : 0), "r"(DESC_HI), "r"(e)
+      "r"(alo), "r"(blo), "r"(idesc), "r"(acc), "r"(DESC_HI), "r"(e)
       : "memory");
 }
-template <bool ACC>
-__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t idesc, uint32_t e) {
+__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t idesc, uint32_t acc,
+                                          uint32_t e) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
       "mov.b64 b, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(blo), "r"(idesc), "n"(ACC ? 1 : 0), "r"(DESC_HI), "r"(e)
+      "r"(a_tmem), "r"(blo), "r"(idesc), "r"(acc), "r"(DESC_HI), "r"(e)
       : "memory");
+}
+// Four K steps (64 of K), A and B advancing by `as` and `bs` a step.
+template <bool TS>
+__device__ __forceinline__ void mma4(uint32_t d, uint32_t a, uint32_t as, uint32_t b, uint32_t bs, uint32_t idesc,
+                                     uint32_t acc, uint32_t e) {
+#pragma unroll
+  for (uint32_t k = 0; k < 4; ++k) {
+    if (TS) mma_ts_lo(d, a + as * k, b + bs * k, idesc, k == 0 ? acc : 1, e);
+    else mma_ss_lo(d, a + as * k, b + bs * k, idesc, k == 0 ? acc : 1, e);
+  }
 }
 __device__ __forceinline__ void commit_one(uint32_t bar, uint32_t e) {
   asm volatile(
@@ -160,14 +181,19 @@ __device__ __forceinline__ bool try_wait_at(uint32_t bar, uint32_t phase) {
 }
 // Bounded wait (a second or so) that also gives up once another thread has (the word at
 // `abort`).
+__device__ __forceinline__ uint32_t clock32() {
+  uint32_t c;
+  asm volatile("mov.u32 %0, %%clock;" : "=r"(c));
+  return c;
+}
 __device__ __forceinline__ bool wait_at(uint32_t bar, uint32_t phase, uint32_t abort) {
-  if (try_wait_at(bar, phase)) return true;
-  const long long start = clock64();
+  if (__builtin_expect(try_wait_at(bar, phase), 1)) return true;
+  const uint32_t start = clock32();
+#pragma unroll 1
   while (!try_wait_at(bar, phase)) {
     uint32_t gave_up;
     asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(gave_up) : "r"(abort) : "memory");
-    if (gave_up) return false;
-    if (clock64() - start > (1ll << 31)) {
+    if (__builtin_expect(gave_up || clock32() - start > 0x80000000u, 0)) {
       asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
       return false;
     }
@@ -237,7 +263,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         const LinRunSel sel) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + (-smem_u32(smem_raw) & 1023u);   // an offset, so that accesses stay shared ones
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform in the compiler's eyes, and so the branches on it
   const int ri = sel.run[blockIdx.x % sel.n];
   const int xh = blockIdx.x / sel.n;
   const int h = xh % p.H, x = xh / p.H;
@@ -255,7 +282,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   using T = Tmem<PHASE1>;
   constexpr int NST = M::NST;
   float *pw = reinterpret_cast<float *>(sm + M::PW), *pw_lo = pw + 65;
-  const uint32_t base = smem_u32(sm), abort = base + M::ABORT;
+  const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(sm), 0), abort = base + M::ABORT;
 
   if (warp == 0) {
     tmem_alloc(reinterpret_cast<uint32_t *>(sm + M::SLOT), TMEM_COLS);
@@ -270,11 +297,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     init(M::READY, 2, NPREP);
     init(M::KV, 2, 1);
     init(M::OUT, 2, 1);
-    init(M::OREAD, 1, NFINISH);
+    init(M::OREAD, 1, NOUT);
     init(M::PF, 1, 1);
     init(M::PREAD, 1, NPREP);
-    init(M::DS, 1, NFINISH);
-    init(M::SOP, 1, NFINISH);
+    init(M::DS, 1, NSTATE);
+    init(M::SOP, 1, NSTATE);
     init(M::DRAIN, 1, 1);
     *reinterpret_cast<uint32_t *>(sm + M::ABORT) = 0;
     fence_mbar_init();
@@ -298,16 +325,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   griddep_launch_dependents();
 
   const int beg = it.g * p.seg, end = min(it.len, beg + p.seg);
-  const int nch = (end - beg + C - 1) / C;
+  const int nch = __shfl_sync(0xffffffffu, (end - beg + C - 1) / C, 0);
   const int page = lin_page(p, it.n);
   // (the chain kernel has written the end state of a sequence with several segments)
   float *const final_page = !PHASE1 && it.nseg == 1 && r.s_final && page >= 0
                                 ? r.s_final + (static_cast<size_t>(page) * p.H + h) * DA * DC : nullptr;
   // a state that leaves in fp32 takes all three terms; one that only makes bf16 outputs, two
-  const bool three = PHASE1 || final_page;
+  const bool three = PHASE1 || __shfl_sync(0xffffffffu, final_page != nullptr, 0);
   const int tail_i = rev ? 0 : nch - 1, tail_n = end - beg - C * (nch - 1);   // the only chunk that may be short
 
-  if (warp == NFINISH + NPREP + 1) {
+  if (warp >= W_MMA) regs_dec<R_CTL>();
+  if (warp > W_COPY) {
+    // idle
+  } else if (warp == W_COPY) {
     // ---------------------------------------------------------------- copies
     if (lane == 0) {
       const CUtensorMap *ma = &maps.m[r.ia], *mb = &maps.m[r.ib], *mc = &maps.m[r.ic];
@@ -338,9 +368,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int j = i > NST ? i - NST : 0; j < i; ++j)
         mbar_wait(reinterpret_cast<uint64_t *>(sm + M::LOAD) + j % NST, (j / NST) & 1);
     }
-  } else if (warp == NFINISH + NPREP) {
+  } else if (warp == W_MMA) {
     // ---------------------------------------------------------------- MMAs
-    const uint32_t e = elect_one();
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t phase) {
       ok = ok && warp_wait_at(base + bar, phase, abort);
@@ -351,12 +380,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (!wait(M::LOAD + 8 * pst.at, pst.phase)) return false;
       tc_fence_after();
       const uint32_t sb = base + M::STAGE * pst.at, alo = desc_lo(sb + M::A, 16), blo = desc_lo(sb + M::B, 16);
+      const uint32_t e = elect_one();
 #pragma unroll
-      for (int kk = 0; kk < DA / 16; ++kk) {
-        const uint32_t o = (kk >> 2) * 512 + (kk & 3) * 2;
-        if (kk == 0) mma_ss_lo<false>(T::P, alo, blo, idesc_bf16(C, C, false, false), e);
-        else mma_ss_lo<true>(T::P, alo + o, blo + o, idesc_bf16(C, C, false, false), e);
-      }
+      for (uint32_t d = 0; d < DA / 64; ++d)
+        mma4<false>(T::P, alo + 512 * d, 2, blo + 512 * d, 2, idesc_bf16(C, C, false, false), d, e);
       commit_one(base + M::PF, e);
       pst.next();
       return true;
@@ -374,45 +401,37 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (i > 0 && !wait(M::DS, one ^ 1)) break;
       tc_fence_after();
       const uint32_t blo = desc_lo(sb + M::B, 8192), wcol = T::term(PHASE1 || !three ? bf.at : 0, 0);
+      {
+        const uint32_t e = elect_one();
 #pragma unroll
-      for (int t = 0; t < 3; ++t)
-        if (t < 2 || three)
-#pragma unroll
-          for (int kk = 0; kk < C / 16; ++kk) {
-            if (t + kk == 0) mma_ts_lo<false>(T::DS, wcol, blo, idesc_bf16(128, DA, false, true), e);
-            else mma_ts_lo<true>(T::DS, wcol + 32 * t + 8 * kk, blo + 128 * kk, idesc_bf16(128, DA, false, true), e);
-          }
-      commit_one(base + M::KV + 8 * bf.at, e);
-      if (PHASE1) {
-        commit_one(base + M::FREE + 8 * st.at, e);
-        continue;
+        for (uint32_t t = 0; t < 2; ++t) mma4<true>(T::DS, wcol + 32 * t, 8, blo, 128, idesc_bf16(128, DA, false, true), t, e);
+        if (three) mma4<true>(T::DS, wcol + 64, 8, blo, 128, idesc_bf16(128, DA, false, true), 1, e);
+        commit_one(base + M::KV + 8 * bf.at, e);
+        if (PHASE1) commit_one(base + M::FREE + 8 * st.at, e);
       }
+      if (PHASE1) continue;
       // O1^T = S^T a^T, O2^T = c^T P^T
       if (!wait(M::SOP, one)) break;
       if (i > 0 && !wait(M::OREAD, one ^ 1)) break;
       tc_fence_after();
-      const uint32_t alo = desc_lo(sb + M::A, 16), clo = desc_lo(sb + M::CT, 8192), plo = desc_lo(base + M::P + 8192 * bf.at, 16);
+      const uint32_t alo = desc_lo(sb + M::A, 16);
+      const uint32_t e = elect_one();
 #pragma unroll
-      for (int kk = 0; kk < DA / 16; ++kk) {
-        const uint32_t a = alo + (kk >> 2) * 512 + (kk & 3) * 2;
-        if (kk == 0) mma_ts_lo<false>(T::O, T::S, a, idesc_bf16(128, C, false, false), e);
-        else mma_ts_lo<true>(T::O, T::S + 8 * kk, a, idesc_bf16(128, C, false, false), e);
-      }
-#pragma unroll
-      for (int kk = 0; kk < C / 16; ++kk) {
-        if (kk == 0) mma_ss_lo<false>(T::O + 64, clo, plo, idesc_bf16(128, C, true, false), e);
-        else mma_ss_lo<true>(T::O + 64, clo + 128 * kk, plo + 2 * kk, idesc_bf16(128, C, true, false), e);
-      }
+      for (uint32_t d = 0; d < DA / 64; ++d)
+        mma4<true>(T::O, T::S + 32 * d, 8, alo + 512 * d, 2, idesc_bf16(128, C, false, false), d, e);
+      mma4<false>(T::O + 64, desc_lo(sb + M::CT, 8192), 128, desc_lo(base + M::P + 8192 * bf.at, 16), 2,
+                  idesc_bf16(128, C, true, false), 0, e);
       commit_one(base + M::OUT + 8 * bf.at, e);
       commit_one(base + M::FREE + 8 * st.at, e);
     }
     if (!ok) {   // a wait gave up: the MMAs in flight finish before the memory they use is released
-      commit_one(base + M::DRAIN, e);
+      commit_one(base + M::DRAIN, elect_one());
       mbar_wait(reinterpret_cast<uint64_t *>(sm + M::DRAIN), 0);
     }
-  } else if (warp >= NFINISH) {
+  } else if (warp >= W_PREP) {
     // ---------------------------------------------------------------- prep: P and w c
-    const int quad = warp & 3, half = (warp - NFINISH) >> 2;
+    regs_dec<R_PREP>();
+    const int quad = warp & 3, half = (warp - W_PREP) >> 2;
     const float bscale = r.bscale;
     const uint32_t lrow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const bool has_c = 32 * quad < DC;
@@ -450,7 +469,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t get1 = base + M::CT + ((dq + 16) >> 6) * 8192 + sw128(sq, ((dq + 16) & 63) >> 3);
     auto weigh = [&](uint32_t stage, uint32_t col, int n, auto terms) {
       constexpr int TERMS = decltype(terms)::value;
-#pragma unroll
+#pragma unroll 1
       for (int g = 0; g < 2; ++g) {
         uint32_t v[8], t1[8], t2[8];
 #pragma unroll
@@ -539,12 +558,113 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       __syncwarp();
       if (lane == 0) arrive_at(base + M::READY + 8 * bf.at);
     }
+  } else if (warp >= W_OUT) {
+    // ---------------------------------------------------------------- output
+    regs_dec<R_OUT>();
+    // this warp's 32 columns dc and 32 tokens t, through its 2 KB of shared memory (rows t of
+    // 64 bytes, 16-byte chunks XOR-ed with t / 2) unless in fp32.  Fragment tiles: lane
+    // holds dc = 16 hh + lane / 4 (+ 8), t = 16 tt + 8 j + 2 (lane % 4) (+ 1).
+    const int quad = warp & 3, half = (warp - W_OUT) >> 2;
+    const uint32_t lrow = tmem + (static_cast<uint32_t>(quad * 32) << 16) + T::O + 32 * half;
+    const float yscale = r.yscale;
+    const size_t ystep = static_cast<size_t>(p.H) * DC;
+    const int tf = 32 * half + 2 * (lane & 3), tr = 32 * half + (lane >> 2);
+    const uint32_t stage = base + M::Y + 2048 * (warp - W_OUT);
+    // stmatrix: matrix m = tokens 8 (m / 2) .., columns 8 (m & 1) ..; its row q = token
+    const int tq = 8 * (lane >> 4) + (lane & 7), cq = (lane >> 3) & 1;
+    const uint32_t put0 = stage + tq * 64 + (((cq ^ (tq >> 1)) & 3) << 4), put1 = stage + tq * 64 + ((((2 + cq) ^ (tq >> 1)) & 3) << 4);
+    const uint32_t get = stage + (lane >> 2) * 64 + ((((lane & 3) ^ (lane >> 3)) & 3) << 4);   // every 512 bytes on: token + 8
+    // full chunks' decays
+    uint64_t gam[4];
+    auto gamma = [&](int n) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = tf + 8 * j;
+        gam[j] = pair_f32(yscale * pw[rev ? max(n - 1 - t, 0) : t + 1], yscale * pw[rev ? max(n - 2 - t, 0) : t + 2]);
+      }
+    };
+    gamma(C);
+    // this lane's row in the chunk, advanced chunk by chunk
+    uint8_t *yrow;
+    const long long yadvance = (rev ? -C : C) * static_cast<long long>(ystep) * (YF32 ? 4 : 2);
+    {
+      const size_t row = static_cast<size_t>(it.b) * p.T + it.t0 + beg + (rev ? C * (nch - 1) : 0);
+      if (YF32) yrow = reinterpret_cast<uint8_t *>(static_cast<float *>(r.y) + (row + tf) * ystep + h * DC + 32 * quad + (lane >> 2));
+      else yrow = reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(r.y) + (row + tr) * ystep + h * DC + 32 * quad + 8 * (lane & 3));
+    }
+    griddep_wait();
+    if (!PHASE1 && 32 * quad < DC) {
+      Ring<2> bf;
+      for (int i = 0; i < nch; ++i, bf.next(), yrow += yadvance) {
+        const int n = i == tail_i ? tail_n : C;
+        if (!warp_wait_at(base + M::OUT + 8 * bf.at, bf.phase, abort)) break;
+        tc_fence_after();
+        if (n < C) gamma(n);
+#pragma unroll 1
+        for (int tt = 0; tt < 2; ++tt) {
+          float v1[2][8], v2[2][8];   // 16 lanes of tensor memory each: dc = 32 quad + 16 hh ..
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            tmem_ld_frag2(lrow + (static_cast<uint32_t>(16 * hh) << 16) + 16 * tt, v1[hh]);
+            tmem_ld_frag2(lrow + (static_cast<uint32_t>(16 * hh) << 16) + 16 * tt + 64, v2[hh]);
+          }
+          tmem_wait_ld();
+          if (tt == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at(base + M::OREAD);
+          }
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t u[2][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                float a, b;
+                unpair_f32(fma_f32x2(tt ? gam[2 + j] : gam[j], pair_f32(v1[hh][4 * j + 2 * k], v1[hh][4 * j + 2 * k + 1]),
+                                     pair_f32(v2[hh][4 * j + 2 * k], v2[hh][4 * j + 2 * k + 1])), a, b);
+                if (YF32) {
+                  float *dst = reinterpret_cast<float *>(yrow) + (16 * tt + 8 * j) * ystep + 16 * hh + 8 * k;
+                  if (tf + 16 * tt + 8 * j < n) dst[0] = a;
+                  if (tf + 16 * tt + 8 * j + 1 < n) dst[ystep] = b;
+                } else {
+                  u[j][k] = pack_bf16x2(a, b);
+                }
+              }
+            if (!YF32) stmatrix4_trans((hh ? put1 : put0) + 1024 * tt, u[0][0], u[0][1], u[1][0], u[1][1]);
+          }
+        }
+        if (!YF32) {
+          __syncwarp();
+          uint4 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ld_shared_v4(get + 512 * k, v[k]);
+          if (n == C) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4 *>(yrow + 16 * k * ystep) = v[k];
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (tr + 8 * k < n) *reinterpret_cast<uint4 *>(yrow + 16 * k * ystep) = v[k];
+          }
+          __syncwarp();   // read before the next chunk's rows are put there
+        }
+        if (n < C) gamma(C);
+      }
+    } else if (!PHASE1 && lane == 0) {
+      for (int i = 0; i < nch; ++i) {   // a value width of 64: nothing to read, in step with the others
+        if (!wait_at(base + M::OUT + 8 * (i & 1), (i >> 1) & 1, abort)) break;
+        arrive_at(base + M::OREAD);
+      }
+    }
   } else {
-    // ---------------------------------------------------------------- finish: the state and the outputs
-    const int quad = warp & 3, part = warp >> 2;
-    // thread (quad, lane, part) holds S[da = part DA/4 + j][dc = 32 quad + lane], in pairs along da
-    constexpr int SN = DA / 4;
-    const int dcr = 32 * quad + lane, da0 = part * SN;
+    // ---------------------------------------------------------------- state
+    regs_inc<R_STATE>();
+    // thread (quad, lane, half) holds S[da = half DA/2 + j][dc = 32 quad + lane], in pairs along da
+    const int quad = warp & 3, half = warp >> 2;
+    constexpr int SN = DA / 2;
+    const int dcr = 32 * quad + lane, da0 = half * SN;
     const bool has_c = dcr < DC;
     uint64_t S[SN / 2];
 #pragma unroll
@@ -576,50 +696,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     ChunkDecay decay;
     decay.init(pw[C], pw_lo[C]);
     auto store_operand = [&]() {   // S^T to tensor memory in bf16 (columns da / 2), and the hand-over
-      uint32_t u[SN / 2];
 #pragma unroll
-      for (int m = 0; m < SN / 2; ++m) {
-        float a, b;
-        unpair_f32(S[m], a, b);
-        u[m] = pack_bf16x2(a, b);
+      for (int q = 0; q < SN / 32; ++q) {
+        uint32_t u[16];
+#pragma unroll
+        for (int m = 0; m < 16; ++m) {
+          float a, b;
+          unpair_f32(S[16 * q + m], a, b);
+          u[m] = pack_bf16x2(a, b);
+        }
+        tmem_st16(lrow + T::S + half * (SN / 2) + 16 * q, u);
       }
-      if constexpr (SN == 32) tmem_st16(lrow + T::S + part * 16, u);
-      else tmem_st8(lrow + T::S + part * 8, u);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_at(base + M::SOP);
     };
     if (!PHASE1) store_operand();
-    // the output: this warp's 32 columns dc and 16 tokens t, through its 1 KB of shared
-    // memory (rows t of 64 bytes, 16-byte chunks XOR-ed with t / 2) unless in fp32.
-    // Fragment tiles: lane holds dc = 16 hh + lane / 4 (+ 8), t = 8 j + 2 (lane % 4) (+ 1).
-    const bool has_y = !PHASE1 && quad * 32 < DC;
-    const float yscale = r.yscale;
-    const size_t ystep = static_cast<size_t>(p.H) * DC;
-    const int tf = 16 * part + 2 * (lane & 3), tr = 16 * part + (lane >> 2);
-    const uint32_t stage = base + M::Y + 1024 * warp;
-    // stmatrix: matrix m = tokens 8 (m / 2) .., columns 8 (m & 1) ..; its row q = token
-    const int tq = 8 * (lane >> 4) + (lane & 7), cq = (lane >> 3) & 1;
-    const uint32_t put0 = stage + tq * 64 + (((cq ^ (tq >> 1)) & 3) << 4), put1 = stage + tq * 64 + ((((2 + cq) ^ (tq >> 1)) & 3) << 4);
-    const uint32_t get = stage + (lane >> 2) * 64 + ((((lane & 3) ^ (lane >> 3)) & 3) << 4);   // and 512 bytes on: token + 8
-    // row tr's address in this chunk, advanced chunk by chunk; full chunks' decays
-    uint8_t *yrow = nullptr;
-    const long long yadvance = (rev ? -C : C) * static_cast<long long>(ystep) * (YF32 ? 4 : 2);
-    uint64_t gam[2] = {0, 0};
-    auto gamma = [&](int n, uint64_t (&g)[2]) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int t = tf + 8 * j;
-        g[j] = pair_f32(yscale * pw[rev ? max(n - 1 - t, 0) : t + 1], yscale * pw[rev ? max(n - 2 - t, 0) : t + 2]);
-      }
-    };
-    if (has_y && nch > 0) {
-      const size_t row = static_cast<size_t>(it.b) * p.T + it.t0 + beg + (rev ? C * (nch - 1) : 0);
-      if (YF32) yrow = reinterpret_cast<uint8_t *>(static_cast<float *>(r.y) + (row + tf) * ystep + h * DC + 32 * quad + (lane >> 2));
-      else yrow = reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(r.y) + (row + tr) * ystep + h * DC + 32 * quad + 8 * (lane & 3));
-      gamma(C, gam);
-    }
     bool ok = true;
     Ring<2> bf;
     for (int i = 0; i < nch; ++i, bf.next()) {
@@ -631,87 +724,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const float g = n == C ? decay.next() : pw[n];
         const uint64_t g2 = pair_f32(g, g);
 #pragma unroll
-        for (int q = 0; q < SN / 16; ++q) {
-          float v[16];
-          tmem_ld16(lrow + T::DS + da0 + 16 * q, v);
-          tmem_wait_ld();
+        for (int q = 0; q < SN / 32; ++q) {
+          float v[32];
+          tmem_ld32(lrow + T::DS + da0 + 32 * q, v);
+          if (q == SN / 32 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at(base + M::DS);
+          }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) S[8 * q + e] = fma_f32x2(g2, S[8 * q + e], pair_f32(v[2 * e], v[2 * e + 1]));
+          for (int e = 0; e < 16; ++e) S[16 * q + e] = fma_f32x2(g2, S[16 * q + e], pair_f32(v[2 * e], v[2 * e + 1]));
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_at(base + M::DS);
-      if (PHASE1) continue;
-
       // its operand for the next chunk, once O1^T has been formed from this one's
+      if (PHASE1 || i + 1 == nch) continue;
       if (!(ok = warp_wait_at(base + M::OUT + 8 * bf.at, bf.phase, abort))) break;
       tc_fence_after();
-      if (i + 1 < nch) store_operand();
-      if (!has_y) {
-        if (lane == 0) arrive_at(base + M::OREAD);
-        continue;
-      }
-      if (n < C) gamma(n, gam);
-      const uint32_t col = lrow + T::O + 16 * part;
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {   // 16 lanes of tensor memory: dc = 32 quad + 16 hh ..
-        float v1[8], v2[8];
-        const uint32_t at = col + (static_cast<uint32_t>(16 * hh) << 16);
-        tmem_ld_frag2(at, v1);
-        tmem_ld_frag2(at + 64, v2);
-        tmem_wait_ld();
-        if (hh == 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_at(base + M::OREAD);
-        }
-        uint64_t y[2][2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            y[j][k] = fma_f32x2(gam[j], pair_f32(v1[4 * j + 2 * k], v1[4 * j + 2 * k + 1]),
-                                pair_f32(v2[4 * j + 2 * k], v2[4 * j + 2 * k + 1]));
-        float a, b;
-        if constexpr (YF32) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float *dst = reinterpret_cast<float *>(yrow) + 8 * j * ystep + 16 * hh + 8 * k;
-              unpair_f32(y[j][k], a, b);
-              if (tf + 8 * j < n) dst[0] = a;
-              if (tf + 8 * j + 1 < n) dst[ystep] = b;
-            }
-        } else {
-          uint32_t u[2][2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              unpair_f32(y[j][k], a, b);
-              u[j][k] = pack_bf16x2(a, b);
-            }
-          stmatrix4_trans(hh ? put1 : put0, u[0][0], u[0][1], u[1][0], u[1][1]);
-        }
-      }
-      if constexpr (!YF32) {
-        __syncwarp();
-        uint4 v0, v1;
-        ld_shared_v4(get, v0);
-        ld_shared_v4(get + 512, v1);
-        if (n == C) {
-          *reinterpret_cast<uint4 *>(yrow) = v0;
-          *reinterpret_cast<uint4 *>(yrow + 16 * ystep) = v1;
-        } else {
-          if (tr < n) *reinterpret_cast<uint4 *>(yrow) = v0;
-          if (tr + 8 < n) *reinterpret_cast<uint4 *>(yrow + 16 * ystep) = v1;
-        }
-        __syncwarp();   // read before the next chunk's rows are put there
-      }
-      if (n < C) gamma(C, gam);
-      yrow += yadvance;
+      store_operand();
     }
     float *dst = PHASE1 ? r.X + (static_cast<size_t>(x) * p.H + h) * DA * DC : final_page;
     if (dst && has_c && ok) {
