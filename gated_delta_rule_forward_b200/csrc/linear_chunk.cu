@@ -29,10 +29,10 @@
 // One CTA has the SM.  Its warps are specialised and hand over through
 // mbarriers, so that three chunks are under way at once:
 //     copies (1 warp)    a, b, c of the chunks to come, each into the stage of one that is done
-//     prep   (8 warps)   P and w c of chunk i + 1
+//     prep   (8 warps)   w c of chunk i + 1
 //     MMAs   (1 warp)    dS(i), P(i + 1), O1(i), O2(i)
 //     state  (8 warps)   S after chunk i, its bf16 operand
-//     output (8 warps)   the rows of chunk i
+//     output (8 warps)   P of chunk i + 1 to bf16, the rows of chunk i
 // Only S -> operand -> O1 is a chain from chunk to chunk.
 #include <type_traits>
 
@@ -78,14 +78,15 @@ struct Smem {
   static constexpr uint32_t LOAD = BAR;              // a, b and c landed
   static constexpr uint32_t FREE = LOAD + 8 * NST;   // every MMA that reads them complete
   // per buffer of two
-  static constexpr uint32_t READY = FREE + 8 * NST;  // P and w c written (8 warps)
+  static constexpr uint32_t READY = FREE + 8 * NST;  // w c written (8 warps)
   static constexpr uint32_t KV = READY + 16;         // dS^T formed
   static constexpr uint32_t OUT = KV + 16;           // O1^T and O2^T formed
   // one each
   static constexpr uint32_t OREAD = OUT + 16;        // O1^T and O2^T read (8 warps)
-  static constexpr uint32_t PF = OREAD + 8;          // P formed
-  static constexpr uint32_t PREAD = PF + 8;          // P read (8 warps)
-  static constexpr uint32_t DS = PREAD + 8;          // dS^T read (8 warps)
+  static constexpr uint32_t PREAD = OREAD + 8;       // P read (8 warps)
+  static constexpr uint32_t PBF = PREAD + 8;         // two: P written in bf16 (8 warps)
+  static constexpr uint32_t PF = PBF + 16;           // two: P formed
+  static constexpr uint32_t DS = PF + 16;            // dS^T read (8 warps)
   static constexpr uint32_t SOP = DS + 8;            // S^T of the chunk's start in tensor memory (8 warps)
   static constexpr uint32_t DRAIN = SOP + 8;
   static constexpr uint32_t SLOT = DRAIN + 8;        // tensor-memory address
@@ -298,8 +299,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     init(M::KV, 2, 1);
     init(M::OUT, 2, 1);
     init(M::OREAD, 1, NOUT);
-    init(M::PF, 1, 1);
-    init(M::PREAD, 1, NPREP);
+    init(M::PF, 2, 1);
+    init(M::PREAD, 1, NOUT);
+    init(M::PBF, 2, NOUT);
     init(M::DS, 1, NSTATE);
     init(M::SOP, 1, NSTATE);
     init(M::DRAIN, 1, 1);
@@ -376,6 +378,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       return ok;
     };
     Ring<NST> pst;   // of the chunk whose P is formed next
+    Ring<2> pbf;
     auto issue_p = [&]() -> bool {   // P = a b^T once both landed
       if (!wait(M::LOAD + 8 * pst.at, pst.phase)) return false;
       tc_fence_after();
@@ -384,8 +387,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
       for (uint32_t d = 0; d < DA / 64; ++d)
         mma4<false>(T::P, alo + 512 * d, 2, blo + 512 * d, 2, idesc_bf16(C, C, false, false), d, e);
-      commit_one(base + M::PF, e);
+      commit_one(base + M::PF + 8 * pbf.at, e);
       pst.next();
+      pbf.next();
       return true;
     };
     if (!PHASE1 && nch > 0) issue_p();
@@ -413,6 +417,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // O1^T = S^T a^T, O2^T = c^T P^T
       if (!wait(M::SOP, one)) break;
       if (i > 0 && !wait(M::OREAD, one ^ 1)) break;
+      if (!wait(M::PBF + 8 * bf.at, bf.phase)) break;
       tc_fence_after();
       const uint32_t alo = desc_lo(sb + M::A, 16);
       const uint32_t e = elect_one();
@@ -429,30 +434,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       mbar_wait(reinterpret_cast<uint64_t *>(sm + M::DRAIN), 0);
     }
   } else if (warp >= W_PREP) {
-    // ---------------------------------------------------------------- prep: P and w c
+    // ---------------------------------------------------------------- prep: w c
     regs_dec<R_PREP>();
     const int quad = warp & 3, half = (warp - W_PREP) >> 2;
     const float bscale = r.bscale;
-    const uint32_t lrow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const bool has_c = 32 * quad < DC;
     const int s0 = 32 * half + 2 * (lane & 3);   // this thread's tokens: s0 + 8 j (+ 1), j = 0 .. 3
-    // P: rows t = 16 quad + lane / 4 (+ 8), columns s0 + 8 j (+ 1); the decays are the same for every chunk
-    uint64_t dec[4][2];
-    if (!PHASE1) {
-      const float f = bscale * r.yscale;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int t = 16 * quad + (lane >> 2) + 8 * k, s = s0 + 8 * j;
-          const int d = rev ? s - t : t - s, d1 = rev ? d + 1 : d - 1;
-          dec[j][k] = pair_f32(d >= 0 ? f * pw[max(d, 0)] : 0.f, d1 >= 0 ? f * pw[max(d1, 0)] : 0.f);
-        }
-    }
-    // stmatrix of P: matrix m = rows 8 (m & 1) .., columns 8 (m / 2) ..
-    const int tp = 16 * quad + (lane & 15), cp = 4 * half + (lane >> 4);
-    const uint32_t put0 = base + M::P + sw128(tp, cp), put1 = base + M::P + sw128(tp, cp + 2);
-    // w c: lanes dc = 32 quad + 16 g + lane / 4 (+ 8), tokens s0 + 8 j (+ 1)
+    // w c: lanes dc = 32 quad + 16 g + lane / 4 (+ 8), tokens s0 + 8 j (+ 1); full chunks' weights
     float wgt[4][2];
     auto weights = [&](int n) {
 #pragma unroll
@@ -469,27 +457,32 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t get1 = base + M::CT + ((dq + 16) >> 6) * 8192 + sw128(sq, ((dq + 16) & 63) >> 3);
     auto weigh = [&](uint32_t stage, uint32_t col, int n, auto terms) {
       constexpr int TERMS = decltype(terms)::value;
-#pragma unroll 1
-      for (int g = 0; g < 2; ++g) {
-        uint32_t v[8], t1[8], t2[8];
+      uint32_t v[2][8];
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
 #pragma unroll
         for (int j = 0; j < 4; j += 2)
-          ldmatrix4_trans((g ? get1 : get0) + stage + 1024 * j, v[2 * j], v[2 * j + 1], v[2 * j + 2], v[2 * j + 3]);
-        if (n < C)   // tokens behind the sequence's end count for nothing, whatever they hold
+          ldmatrix4_trans((g ? get1 : get0) + stage + 1024 * j, v[g][2 * j], v[g][2 * j + 1], v[g][2 * j + 2], v[g][2 * j + 3]);
+      if (n < C)   // tokens behind the sequence's end count for nothing, whatever they hold
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int s = s0 + 8 * (j >> 1);
-            v[j] &= s + 1 < n ? 0xffffffffu : s < n ? 0xffffu : 0u;
-          }
+        for (int j = 0; j < 8; ++j) {
+          const int s = s0 + 8 * (j >> 1);
+          const uint32_t keep = s + 1 < n ? 0xffffffffu : s < n ? 0xffffu : 0u;
+          v[0][j] &= keep;
+          v[1][j] &= keep;
+        }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) split_pair<TERMS>(v[j], wgt[j >> 1][0], wgt[j >> 1][1], v[j], t1[j], t2[j]);
+      for (int g = 0; g < 2; ++g) {
+        uint32_t t1[8], t2[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) split_pair<TERMS>(v[g][j], wgt[j >> 1][0], wgt[j >> 1][1], v[g][j], t1[j], t2[j]);
         const uint32_t at = col + (static_cast<uint32_t>(16 * g) << 16);
-        tmem_st_frag4(at, v);
+        tmem_st_frag4(at, v[g]);
         tmem_st_frag4(at + 32, t1);
         if (TERMS == 3) tmem_st_frag4(at + 64, t2);
       }
     };
-    const uint32_t wlane = lrow + 16 * half;
+    const uint32_t wlane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 16 * half;
     if (!has_c) {   // value widths of 64: the upper lanes' operand is zero
       const uint32_t zero[8] = {};
       for (int t = 0; t < (PHASE1 ? 8 : 4); ++t)   // every column of the buffers
@@ -500,37 +493,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int i = 0; i < nch; ++i, st.next(), bf.next()) {
       const int n = i == tail_i ? tail_n : C;
       if (!warp_wait_at(base + M::LOAD + 8 * st.at, st.phase, abort)) break;
-      // this chunk's buffers are those of the products of two chunks ago
-      if (i >= 2 && !warp_wait_at(base + (PHASE1 ? M::KV : M::OUT) + 8 * bf.at, bf.phase ^ 1, abort)) break;
-      if (!PHASE1) {
-        if (!warp_wait_at(base + M::PF, i & 1, abort)) break;
-        tc_fence_after();
-        float v[16];
-        tmem_ld_frag4(lrow + T::P + 32 * half, v);
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_at(base + M::PREAD);
-        uint32_t u[4][2];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float y0, y1;
-            unpair_f32(mul_f32x2(pair_f32(v[4 * j + 2 * k], v[4 * j + 2 * k + 1]), dec[j][k]), y0, y1);
-            u[j][k] = pack_bf16x2(y0, y1);
-          }
-        if (n < C)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t keep = s0 + 8 * j + 1 < n ? 0xffffffffu : s0 + 8 * j < n ? 0xffffu : 0u;
-            u[j][0] &= keep;
-            u[j][1] &= keep;
-          }
-        stmatrix4(put0 + 8192 * bf.at, u[0][0], u[0][1], u[1][0], u[1][1]);
-        stmatrix4(put1 + 8192 * bf.at, u[2][0], u[2][1], u[3][0], u[3][1]);
-        // one buffer of three terms: the last chunk's product has to be complete
-        if (three && i >= 1 && !warp_wait_at(base + M::KV + 8 * (bf.at ^ 1), bf.phase ^ (bf.at ^ 1), abort)) break;
+      // the buffer is that of the product of two chunks ago (one buffer of three terms: of the last chunk)
+      if (!PHASE1 && three) {
+        if (i >= 1 && !warp_wait_at(base + M::KV + 8 * (bf.at ^ 1), bf.phase ^ (bf.at ^ 1), abort)) break;
+      } else {
+        if (i >= 2 && !warp_wait_at(base + M::KV + 8 * bf.at, bf.phase ^ 1, abort)) break;
       }
       tc_fence_after();
       if (n < C) weights(n);
@@ -542,7 +509,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       tmem_wait_st();
       if (n < C) {
         // rows behind the sequence's end, which the products read as well, become zeros (once all of c is
-        // read; P has been formed, and is cleared of them above)
+        // read and P is formed; the output warps clear P of them)
+        if (!PHASE1 && !warp_wait_at(base + M::PF + 8 * bf.at, bf.phase, abort)) break;
         named_bar_sync(1, 32 * NPREP);
         uint8_t *sb = sm + M::STAGE * st.at;
         const int row = tid & 63, piece = (tid >> 6) & 3;
@@ -552,14 +520,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           for (int j = piece; j < DC / 8; j += 4) *reinterpret_cast<uint4 *>(sb + M::CT + (j >> 3) * 8192 + sw128(row, j & 7)) = zero;
         }
         weights(C);
+        fence_async_smem();
       }
-      fence_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_at(base + M::READY + 8 * bf.at);
     }
   } else if (warp >= W_OUT) {
-    // ---------------------------------------------------------------- output
+    // ---------------------------------------------------------------- P and the output
     regs_dec<R_OUT>();
     // this warp's 32 columns dc and 32 tokens t, through its 2 KB of shared memory (rows t of
     // 64 bytes, 16-byte chunks XOR-ed with t / 2) unless in fp32.  Fragment tiles: lane
@@ -592,71 +560,123 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (YF32) yrow = reinterpret_cast<uint8_t *>(static_cast<float *>(r.y) + (row + tf) * ystep + h * DC + 32 * quad + (lane >> 2));
       else yrow = reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(r.y) + (row + tr) * ystep + h * DC + 32 * quad + 8 * (lane & 3));
     }
+    // P: rows t = 16 quad + lane / 4 (+ 8), columns s0 + 8 j (+ 1); the decays are the same for every chunk
+    const int s0 = tf;
+    uint64_t dec[4][2];
+    {
+      const float f = r.bscale * yscale;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int t = 16 * quad + (lane >> 2) + 8 * k, s = s0 + 8 * j;
+          const int d = rev ? s - t : t - s, d1 = rev ? d + 1 : d - 1;
+          dec[j][k] = pair_f32(d >= 0 ? f * pw[max(d, 0)] : 0.f, d1 >= 0 ? f * pw[max(d1, 0)] : 0.f);
+        }
+    }
+    // stmatrix of P: matrix m = rows 8 (m & 1) .., columns 8 (m / 2) ..
+    const int tp = 16 * quad + (lane & 15), cp = 4 * half + (lane >> 4);
+    const uint32_t pput0 = base + M::P + sw128(tp, cp), pput1 = base + M::P + sw128(tp, cp + 2);
+    const uint32_t plane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + T::P + 32 * half;
     griddep_wait();
-    if (!PHASE1 && 32 * quad < DC) {
-      Ring<2> bf;
-      for (int i = 0; i < nch; ++i, bf.next(), yrow += yadvance) {
+    Ring<2> bf, obf;   // of P's chunk, and of the output's, one behind
+    for (int i = 0; !PHASE1 && i <= nch; ++i, bf.next()) {
+      if (i < nch) {   // P of chunk i, with its decays
         const int n = i == tail_i ? tail_n : C;
-        if (!warp_wait_at(base + M::OUT + 8 * bf.at, bf.phase, abort)) break;
+        if (!warp_wait_at(base + M::PF + 8 * bf.at, bf.phase, abort)) break;
         tc_fence_after();
-        if (n < C) gamma(n);
-#pragma unroll 1
-        for (int tt = 0; tt < 2; ++tt) {
-          float v1[2][8], v2[2][8];   // 16 lanes of tensor memory each: dc = 32 quad + 16 hh ..
+        float v[16];
+        tmem_ld_frag4(plane, v);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_at(base + M::PREAD);
+        uint32_t u[4][2];
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            tmem_ld_frag2(lrow + (static_cast<uint32_t>(16 * hh) << 16) + 16 * tt, v1[hh]);
-            tmem_ld_frag2(lrow + (static_cast<uint32_t>(16 * hh) << 16) + 16 * tt + 64, v2[hh]);
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float y0, y1;
+            unpair_f32(mul_f32x2(pair_f32(v[4 * j + 2 * k], v[4 * j + 2 * k + 1]), dec[j][k]), y0, y1);
+            u[j][k] = pack_bf16x2(y0, y1);
           }
-          tmem_wait_ld();
-          if (tt == 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_at(base + M::OREAD);
+        if (n < C)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t keep = s0 + 8 * j + 1 < n ? 0xffffffffu : s0 + 8 * j < n ? 0xffffu : 0u;
+            u[j][0] &= keep;
+            u[j][1] &= keep;
           }
+        // (the buffer's last reader, the product of two chunks ago, was waited for with its output)
+        stmatrix4(pput0 + 8192 * bf.at, u[0][0], u[0][1], u[1][0], u[1][1]);
+        stmatrix4(pput1 + 8192 * bf.at, u[2][0], u[2][1], u[3][0], u[3][1]);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_at(base + M::PBF + 8 * bf.at);
+      }
+      if (i == 0) continue;
+      // the output of chunk i - 1
+      const int n = i - 1 == tail_i ? tail_n : C;
+      if (!warp_wait_at(base + M::OUT + 8 * obf.at, obf.phase, abort)) break;
+      tc_fence_after();
+      obf.next();
+      if (32 * quad >= DC) {   // a value width of 64: nothing of it in these lanes
+        if (lane == 0) arrive_at(base + M::OREAD);
+        continue;
+      }
+      if (n < C) gamma(n);
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            uint32_t u[2][2];
+      for (int tt = 0; tt < 2; ++tt) {
+        float v1[2][8], v2[2][8];   // 16 lanes of tensor memory each: dc = 32 quad + 16 hh ..
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                float a, b;
-                unpair_f32(fma_f32x2(tt ? gam[2 + j] : gam[j], pair_f32(v1[hh][4 * j + 2 * k], v1[hh][4 * j + 2 * k + 1]),
-                                     pair_f32(v2[hh][4 * j + 2 * k], v2[hh][4 * j + 2 * k + 1])), a, b);
-                if (YF32) {
-                  float *dst = reinterpret_cast<float *>(yrow) + (16 * tt + 8 * j) * ystep + 16 * hh + 8 * k;
-                  if (tf + 16 * tt + 8 * j < n) dst[0] = a;
-                  if (tf + 16 * tt + 8 * j + 1 < n) dst[ystep] = b;
-                } else {
-                  u[j][k] = pack_bf16x2(a, b);
-                }
-              }
-            if (!YF32) stmatrix4_trans((hh ? put1 : put0) + 1024 * tt, u[0][0], u[0][1], u[1][0], u[1][1]);
-          }
+        for (int hh = 0; hh < 2; ++hh) {
+          tmem_ld_frag2(lrow + (static_cast<uint32_t>(16 * hh) << 16) + 16 * tt, v1[hh]);
+          tmem_ld_frag2(lrow + (static_cast<uint32_t>(16 * hh) << 16) + 16 * tt + 64, v2[hh]);
         }
-        if (!YF32) {
+        tmem_wait_ld();
+        if (tt == 1) {
+          tc_fence_before();
           __syncwarp();
-          uint4 v[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) ld_shared_v4(get + 512 * k, v[k]);
-          if (n == C) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4 *>(yrow + 16 * k * ystep) = v[k];
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (tr + 8 * k < n) *reinterpret_cast<uint4 *>(yrow + 16 * k * ystep) = v[k];
-          }
-          __syncwarp();   // read before the next chunk's rows are put there
+          if (lane == 0) arrive_at(base + M::OREAD);
         }
-        if (n < C) gamma(C);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t u[2][2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float a, b;
+              unpair_f32(fma_f32x2(gam[2 * tt + j], pair_f32(v1[hh][4 * j + 2 * k], v1[hh][4 * j + 2 * k + 1]),
+                                   pair_f32(v2[hh][4 * j + 2 * k], v2[hh][4 * j + 2 * k + 1])), a, b);
+              if (YF32) {
+                float *dst = reinterpret_cast<float *>(yrow) + (16 * tt + 8 * j) * ystep + 16 * hh + 8 * k;
+                if (tf + 16 * tt + 8 * j < n) dst[0] = a;
+                if (tf + 16 * tt + 8 * j + 1 < n) dst[ystep] = b;
+              } else {
+                u[j][k] = pack_bf16x2(a, b);
+              }
+            }
+          if (!YF32) stmatrix4_trans((hh ? put1 : put0) + 1024 * tt, u[0][0], u[0][1], u[1][0], u[1][1]);
+        }
       }
-    } else if (!PHASE1 && lane == 0) {
-      for (int i = 0; i < nch; ++i) {   // a value width of 64: nothing to read, in step with the others
-        if (!wait_at(base + M::OUT + 8 * (i & 1), (i >> 1) & 1, abort)) break;
-        arrive_at(base + M::OREAD);
+      if (!YF32) {
+        __syncwarp();
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ld_shared_v4(get + 512 * k, v[k]);
+        if (n == C) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4 *>(yrow + 16 * k * ystep) = v[k];
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (tr + 8 * k < n) *reinterpret_cast<uint4 *>(yrow + 16 * k * ystep) = v[k];
+        }
+        __syncwarp();   // read before the next chunk's rows are put there
       }
+      if (n < C) gamma(C);
+      yrow += yadvance;
     }
   } else {
     // ---------------------------------------------------------------- state
