@@ -30,7 +30,7 @@
 // mbarriers, so that three chunks are under way at once:
 //     copies (1 warp)    a, b, c of the chunks to come, each into the stage of one that is done
 //     prep   (8 warps)   w c of chunk i + 1
-//     MMAs   (1 warp)    dS(i), P(i + 1), O1(i), O2(i)
+//     MMAs   (3 warps)   P(i + 1);  dS(i);  O1(i), O2(i)
 //     state  (8 warps)   S after chunk i, its bf16 operand
 //     output (8 warps)   P of chunk i + 1 to bf16, the rows of chunk i
 // Only S -> operand -> O1 is a chain from chunk to chunk.
@@ -49,13 +49,14 @@ namespace tc {
 namespace {
 
 constexpr int C = 64;
-// warps 0-7 state, 8-15 output, 16-23 prep, then the MMA and the copy warp (and two idle
-// ones that complete their warpgroup)
+// warps 0-7 state, 8-15 output, 16-23 prep, then one for the copies and one for each of
+// the three kinds of products
 constexpr int NSTATE = 8, NOUT = 8, NPREP = 8;
-constexpr int W_OUT = NSTATE, W_PREP = W_OUT + NOUT, W_MMA = W_PREP + NPREP, W_COPY = W_MMA + 1;
-constexpr int NTHREADS = 32 * (W_MMA + 4);
+constexpr int W_OUT = NSTATE, W_PREP = W_OUT + NOUT, W_COPY = W_PREP + NPREP, W_MMA_P = W_COPY + 1, W_MMA_DS = W_COPY + 2,
+              W_MMA_O = W_COPY + 3;
+constexpr int NTHREADS = 32 * (W_COPY + 4);
 // registers a thread: 72 at launch, moved to the threads that hold the state
-constexpr int R_STATE = 112, R_OUT = 64, R_PREP = 64, R_CTL = 24;
+constexpr int R_STATE = 112, R_OUT = 64, R_PREP = 56, R_CTL = 40;
 static_assert(32 * (NSTATE * R_STATE + NOUT * R_OUT + NPREP * R_PREP + 4 * R_CTL) <= 72 * NTHREADS, "register split");
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -76,7 +77,7 @@ struct Smem {
   static constexpr uint32_t BAR = PW + 2 * 65 * 4 + 8;
   // barriers per stage
   static constexpr uint32_t LOAD = BAR;              // a, b and c landed
-  static constexpr uint32_t FREE = LOAD + 8 * NST;   // every MMA that reads them complete
+  static constexpr uint32_t FREE = LOAD + 8 * NST;   // the products that read them complete (dS^T; O1^T and O2^T, which P came before)
   // per buffer of two
   static constexpr uint32_t READY = FREE + 8 * NST;  // w c written (8 warps)
   static constexpr uint32_t KV = READY + 16;         // dS^T formed
@@ -86,10 +87,11 @@ struct Smem {
   static constexpr uint32_t PREAD = OREAD + 8;       // P read (8 warps)
   static constexpr uint32_t PBF = PREAD + 8;         // two: P written in bf16 (8 warps)
   static constexpr uint32_t PF = PBF + 16;           // two: P formed
-  static constexpr uint32_t DS = PF + 16;            // dS^T read (8 warps)
-  static constexpr uint32_t SOP = DS + 8;            // S^T of the chunk's start in tensor memory (8 warps)
+  static constexpr uint32_t DS = PF + 16;            // two: dS^T read (8 warps)
+  static constexpr uint32_t SOP = DS + 16;           // S^T of the chunk's start in tensor memory (8 warps)
   static constexpr uint32_t DRAIN = SOP + 8;
-  static constexpr uint32_t SLOT = DRAIN + 8;        // tensor-memory address
+  static constexpr uint32_t PTAIL = DRAIN + 24;      // P of the short chunk formed (once)
+  static constexpr uint32_t SLOT = PTAIL + 8;        // tensor-memory address
   static constexpr uint32_t ABORT = SLOT + 4;        // a wait gave up
   static constexpr uint32_t BYTES = ABORT + 4 + 1024;
   static_assert(BAR % 16 == 0 && P % 1024 == 0 && BYTES <= 232448, "one CTA per SM");
@@ -97,13 +99,13 @@ struct Smem {
 // Tensor memory columns.
 template <bool PHASE1>
 struct Tmem {
-  static constexpr uint32_t DS = 0;      // dS^T, 128
+  static constexpr uint32_t DS = 0;      // dS^T, 128 (phase 1: two buffers)
   static constexpr uint32_t S = 128;     // S^T in bf16, 64
   static constexpr uint32_t P = 192;     // P, 64
   static constexpr uint32_t O = 256;     // O1^T and O2^T, 64 each
   // (w c)^T in bf16, 32 columns a term: two buffers of two terms (phase 1: of three);
   // beside the outputs there is room for one buffer of three
-  static constexpr uint32_t W = PHASE1 ? 128 : 384;
+  static constexpr uint32_t W = PHASE1 ? 256 : 384;
   __device__ static constexpr uint32_t term(int buf, int t) { return W + (PHASE1 ? 128 : 64) * buf + 32 * t; }
 };
 constexpr uint32_t TMEM_COLS = 512;
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int i = 0; i < n; ++i) mbar_init(reinterpret_cast<uint64_t *>(sm + at + 8 * i), count);
     };
     init(M::LOAD, NST, 1);
-    init(M::FREE, NST, 1);
+    init(M::FREE, NST, PHASE1 ? 1 : 2);
     init(M::READY, 2, NPREP);
     init(M::KV, 2, 1);
     init(M::OUT, 2, 1);
@@ -302,9 +304,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     init(M::PF, 2, 1);
     init(M::PREAD, 1, NOUT);
     init(M::PBF, 2, NOUT);
-    init(M::DS, 1, NSTATE);
+    init(M::DS, 2, NSTATE);
     init(M::SOP, 1, NSTATE);
-    init(M::DRAIN, 1, 1);
+    init(M::DRAIN, 3, 1);
+    init(M::PTAIL, 1, 1);
     *reinterpret_cast<uint32_t *>(sm + M::ABORT) = 0;
     fence_mbar_init();
   }
@@ -336,10 +339,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const bool three = PHASE1 || __shfl_sync(0xffffffffu, final_page != nullptr, 0);
   const int tail_i = rev ? 0 : nch - 1, tail_n = end - beg - C * (nch - 1);   // the only chunk that may be short
 
-  if (warp >= W_MMA) regs_dec<R_CTL>();
-  if (warp > W_COPY) {
-    // idle
-  } else if (warp == W_COPY) {
+  if (warp >= W_COPY) regs_dec<R_CTL>();
+  if (warp == W_COPY) {
     // ---------------------------------------------------------------- copies
     if (lane == 0) {
       const CUtensorMap *ma = &maps.m[r.ia], *mb = &maps.m[r.ib], *mc = &maps.m[r.ic];
@@ -370,68 +371,69 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int j = i > NST ? i - NST : 0; j < i; ++j)
         mbar_wait(reinterpret_cast<uint64_t *>(sm + M::LOAD) + j % NST, (j / NST) & 1);
     }
-  } else if (warp == W_MMA) {
+  } else if (warp > W_COPY) {
     // ---------------------------------------------------------------- MMAs
+    // A warp for each kind, so that none waits behind another's operands; a product's
+    // operands are all handed over through barriers, so their order needs no more.
+    // No barrier may complete a phase that some waiter has not yet seen: each waiter of
+    // phase k of a barrier comes, by some chain of hand-overs, before its phase k + 1.
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t phase) {
       ok = ok && warp_wait_at(base + bar, phase, abort);
       return ok;
     };
-    Ring<NST> pst;   // of the chunk whose P is formed next
-    Ring<2> pbf;
-    auto issue_p = [&]() -> bool {   // P = a b^T once both landed
-      if (!wait(M::LOAD + 8 * pst.at, pst.phase)) return false;
-      tc_fence_after();
-      const uint32_t sb = base + M::STAGE * pst.at, alo = desc_lo(sb + M::A, 16), blo = desc_lo(sb + M::B, 16);
-      const uint32_t e = elect_one();
-#pragma unroll
-      for (uint32_t d = 0; d < DA / 64; ++d)
-        mma4<false>(T::P, alo + 512 * d, 2, blo + 512 * d, 2, idesc_bf16(C, C, false, false), d, e);
-      commit_one(base + M::PF + 8 * pbf.at, e);
-      pst.next();
-      pbf.next();
-      return true;
-    };
-    if (!PHASE1 && nch > 0) issue_p();
     Ring<NST> st;
     Ring<2> bf;
-    for (int i = 0; ok && i < nch; ++i, st.next(), bf.next()) {
-      const uint32_t sb = base + M::STAGE * st.at, one = i & 1;
-      // the next chunk's P, as soon as this one's is read
-      if (!PHASE1 && i + 1 < nch && (!wait(M::PREAD, one) || !issue_p())) break;
-      // dS^T = (w c)^T b
-      if (PHASE1 && !wait(M::LOAD + 8 * st.at, st.phase)) break;
-      if (!wait(M::READY + 8 * bf.at, bf.phase)) break;
-      if (i > 0 && !wait(M::DS, one ^ 1)) break;
-      tc_fence_after();
-      const uint32_t blo = desc_lo(sb + M::B, 8192), wcol = T::term(PHASE1 || !three ? bf.at : 0, 0);
-      {
+    if (warp == W_MMA_P) {   // P = a b^T, as soon as the chunk before's is read
+      for (int i = 0; !PHASE1 && i < nch; ++i, st.next(), bf.next()) {
+        if (i > 0 && !wait(M::PREAD, (i - 1) & 1)) break;
+        if (!wait(M::LOAD + 8 * st.at, st.phase)) break;
+        tc_fence_after();
+        const uint32_t sb = base + M::STAGE * st.at, alo = desc_lo(sb + M::A, 16), blo = desc_lo(sb + M::B, 16);
         const uint32_t e = elect_one();
 #pragma unroll
-        for (uint32_t t = 0; t < 2; ++t) mma4<true>(T::DS, wcol + 32 * t, 8, blo, 128, idesc_bf16(128, DA, false, true), t, e);
-        if (three) mma4<true>(T::DS, wcol + 64, 8, blo, 128, idesc_bf16(128, DA, false, true), 1, e);
-        commit_one(base + M::KV + 8 * bf.at, e);
-        if (PHASE1) commit_one(base + M::FREE + 8 * st.at, e);
+        for (uint32_t d = 0; d < DA / 64; ++d)
+          mma4<false>(T::P, alo + 512 * d, 2, blo + 512 * d, 2, idesc_bf16(C, C, false, false), d, e);
+        commit_one(base + M::PF + 8 * bf.at, e);
+        if (i == tail_i) commit_one(base + M::PTAIL, e);
       }
-      if (PHASE1) continue;
-      // O1^T = S^T a^T, O2^T = c^T P^T
-      if (!wait(M::SOP, one)) break;
-      if (i > 0 && !wait(M::OREAD, one ^ 1)) break;
-      if (!wait(M::PBF + 8 * bf.at, bf.phase)) break;
-      tc_fence_after();
-      const uint32_t alo = desc_lo(sb + M::A, 16);
-      const uint32_t e = elect_one();
+    } else if (warp == W_MMA_DS) {   // dS^T = (w c)^T b
+      for (int i = 0; i < nch; ++i, st.next(), bf.next()) {
+        if (!wait(M::LOAD + 8 * st.at, st.phase) || !wait(M::READY + 8 * bf.at, bf.phase)) break;
+        if (PHASE1 ? i >= 2 && !wait(M::DS + 8 * bf.at, bf.phase ^ 1)
+                   : i >= 1 && !wait(M::DS + 8 * (bf.at ^ 1), bf.phase ^ (bf.at ^ 1))) break;
+        tc_fence_after();
+        const uint32_t blo = desc_lo(base + M::STAGE * st.at + M::B, 8192);
+        const uint32_t wcol = T::term(PHASE1 || !three ? bf.at : 0, 0), ds = T::DS + (PHASE1 ? 128 * bf.at : 0);
+        const uint32_t e = elect_one();
 #pragma unroll
-      for (uint32_t d = 0; d < DA / 64; ++d)
-        mma4<true>(T::O, T::S + 32 * d, 8, alo + 512 * d, 2, idesc_bf16(128, C, false, false), d, e);
-      mma4<false>(T::O + 64, desc_lo(sb + M::CT, 8192), 128, desc_lo(base + M::P + 8192 * bf.at, 16), 2,
-                  idesc_bf16(128, C, true, false), 0, e);
-      commit_one(base + M::OUT + 8 * bf.at, e);
-      commit_one(base + M::FREE + 8 * st.at, e);
+        for (uint32_t t = 0; t < 2; ++t) mma4<true>(ds, wcol + 32 * t, 8, blo, 128, idesc_bf16(128, DA, false, true), t, e);
+        if (three) mma4<true>(ds, wcol + 64, 8, blo, 128, idesc_bf16(128, DA, false, true), 1, e);
+        commit_one(base + M::KV + 8 * bf.at, e);
+        commit_one(base + M::FREE + 8 * st.at, e);
+      }
+    } else {   // O1^T = S^T a^T, O2^T = c^T P^T
+      for (int i = 0; !PHASE1 && i < nch; ++i, st.next(), bf.next()) {
+        if (!wait(M::LOAD + 8 * st.at, st.phase) || !wait(M::PBF + 8 * bf.at, bf.phase)) break;
+        if (i > 0 && !wait(M::OREAD, (i - 1) & 1)) break;
+        if (!wait(M::SOP, i & 1)) break;
+        // the short chunk's rows of c behind the end are zeros once its dS^T is formed
+        if (i == tail_i && tail_n < C && !wait(M::KV + 8 * bf.at, bf.phase)) break;
+        tc_fence_after();
+        const uint32_t sb = base + M::STAGE * st.at, alo = desc_lo(sb + M::A, 16);
+        const uint32_t e = elect_one();
+#pragma unroll
+        for (uint32_t d = 0; d < DA / 64; ++d)
+          mma4<true>(T::O, T::S + 32 * d, 8, alo + 512 * d, 2, idesc_bf16(128, C, false, false), d, e);
+        mma4<false>(T::O + 64, desc_lo(sb + M::CT, 8192), 128, desc_lo(base + M::P + 8192 * bf.at, 16), 2,
+                    idesc_bf16(128, C, true, false), 0, e);
+        commit_one(base + M::OUT + 8 * bf.at, e);
+        commit_one(base + M::FREE + 8 * st.at, e);
+      }
     }
     if (!ok) {   // a wait gave up: the MMAs in flight finish before the memory they use is released
-      commit_one(base + M::DRAIN, elect_one());
-      mbar_wait(reinterpret_cast<uint64_t *>(sm + M::DRAIN), 0);
+      commit_one(base + M::DRAIN + 8 * (warp - W_MMA_P), elect_one());
+      mbar_wait(reinterpret_cast<uint64_t *>(sm + M::DRAIN) + (warp - W_MMA_P), 0);
     }
   } else if (warp >= W_PREP) {
     // ---------------------------------------------------------------- prep: w c
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (n < C) {
         // rows behind the sequence's end, which the products read as well, become zeros (once all of c is
         // read and P is formed; the output warps clear P of them)
-        if (!PHASE1 && !warp_wait_at(base + M::PF + 8 * bf.at, bf.phase, abort)) break;
+        if (!PHASE1 && !warp_wait_at(base + M::PTAIL, 0, abort)) break;
         named_bar_sync(1, 32 * NPREP);
         uint8_t *sb = sm + M::STAGE * st.at;
         const int row = tid & 63, piece = (tid >> 6) & 3;
@@ -746,11 +748,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
         for (int q = 0; q < SN / 32; ++q) {
           float v[32];
-          tmem_ld32(lrow + T::DS + da0 + 32 * q, v);
+          tmem_ld32(lrow + T::DS + (PHASE1 ? 128 * bf.at : 0) + da0 + 32 * q, v);
           if (q == SN / 32 - 1) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_at(base + M::DS);
+            if (lane == 0) arrive_at(base + M::DS + 8 * bf.at);
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e) S[16 * q + e] = fma_f32x2(g2, S[16 * q + e], pair_f32(v[2 * e], v[2 * e + 1]));
