@@ -1,5 +1,6 @@
 // libgdr C ABI: argument validation, kernel selection, launch-error mapping.
 // The operation each entry point performs is specified in include/gdr.h.
+#include <atomic>
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
@@ -397,13 +398,20 @@ gdr_status_t gdr_decode_step(int variant, int dtype, int N, int H, int dk, int d
 
 // ------------------------------------------------------------------ linear attention with a decay per head
 
+// SMs of the current device (a property of the device, looked up once for each).
 static int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+  if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     return 148;   // no device: the B200's, for size queries
   }
+  if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 148;
+  }
+  if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 

@@ -34,6 +34,7 @@
 //     state  (8 warps)   S after chunk i, its bf16 operand
 //     output (8 warps)   P of chunk i + 1 to bf16, the rows of chunk i
 // Only S -> operand -> O1 is a chain from chunk to chunk.
+#include <atomic>
 #include <type_traits>
 
 #include "linear.cuh"
@@ -810,8 +811,16 @@ template <int DA, int DC, bool PHASE1, bool YF32>
 cudaError_t launch(const LinProblem &p, const LinChunkMaps &maps, const LinRunSel &sel, bool pdl, cudaStream_t s) {
   constexpr uint32_t SMEM = Smem<PHASE1>::BYTES;
   auto kern = linear_chunk_kernel<DA, DC, PHASE1, YF32>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  // the kernel's limit on the current device, set by the first call there
+  static std::atomic<unsigned long long> set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (!(set.load(std::memory_order_relaxed) & bit)) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess) return e;
+    set.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long>(p.items) * p.H * sel.n));
   cfg.blockDim = dim3(NTHREADS);

@@ -16,8 +16,15 @@ constexpr int kThreads = 256;
 constexpr int kUnroll = 8;
 constexpr int kBlockVec = kThreads * kUnroll;   // float4 per block
 
+template <int MAX>
+struct Pairs {
+  int n;
+  int src[MAX], dst[MAX];
+};
+
+template <int MAX>
 __global__ void __launch_bounds__(kThreads) state_copy_kernel(float4 *pool, size_t page_vec, int pages, int blocks_per_page,
-                                                               const __grid_constant__ CopyPairs pairs) {
+                                                               const __grid_constant__ Pairs<MAX> pairs) {
   const long x = blockIdx.x;
   const int i = static_cast<int>(x % pairs.n);
   const long y = x / pairs.n;
@@ -50,7 +57,16 @@ cudaError_t gdr_launch_state_copy(float *pool, size_t page_floats, int layers, i
   const size_t vec = page_floats / 4;
   const long per_page = static_cast<long>((vec + kBlockVec - 1) / kBlockVec);
   const long blocks = per_page * layers * pairs.n;
-  state_copy_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(reinterpret_cast<float4 *>(pool), vec, pages,
-                                                                       static_cast<int>(per_page), pairs);
+  auto launch = [&](auto few) {
+    few.n = pairs.n;
+    for (int i = 0; i < pairs.n; ++i) {
+      few.src[i] = pairs.src[i];
+      few.dst[i] = pairs.dst[i];
+    }
+    state_copy_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(reinterpret_cast<float4 *>(pool), vec, pages,
+                                                                         static_cast<int>(per_page), few);
+  };
+  if (pairs.n <= kFewCopyPairs) launch(Pairs<kFewCopyPairs>());
+  else launch(Pairs<kMaxCopyPairs>());
   return cudaGetLastError();
 }

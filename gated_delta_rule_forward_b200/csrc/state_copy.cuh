@@ -12,6 +12,8 @@ struct CopyPairs {
   int src[kMaxCopyPairs];   // -1: zeros
   int dst[kMaxCopyPairs];
 };
+// Up to these go as 256 bytes (a launch with 4 KB of arguments takes the host longer).
+constexpr int kFewCopyPairs = 31;
 
 }  // namespace gdr
 

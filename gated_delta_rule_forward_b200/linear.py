@@ -14,46 +14,62 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import torch
 
 from ._lib import LinearArgs, LinearGrads, check, lib
-from .ops import _DTYPES, _need, _ptr
+from .ops import _DTYPES, _need
 
 __all__ = ["linear_forward", "linear_decode_step", "linear_backward", "copy_states", "StateCache"]
 
 _Stride3 = ctypes.c_longlong * 3
 
 
-@contextlib.contextmanager
+_here = contextlib.nullcontext()
+
+
 def _on(device, stream):
-    """The device made current, and `stream` (None: the device's current one)
-    made torch's current stream, so that what is allocated for a call belongs to
-    the stream the call runs on.  Yields the stream's handle."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-        else:
-            if stream.device != device:
-                raise ValueError(f"stream must be on {device}")
-            with torch.cuda.stream(stream):
-                yield ctypes.c_void_p(stream.cuda_stream)
+    """The context a call allocates and launches in, and the handle of its
+    stream.  Where they are not so already, the device is made current and
+    `stream` (None: the device's current one) torch's current stream, so that
+    what is allocated for a call belongs to the stream the call runs on."""
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)     # current_stream() without the object: 2 us less
+        return _here if device.index == torch.cuda.current_device() else torch.cuda.device(device), handle
+    if stream.device != device:
+        raise ValueError(f"stream must be on {device}")
+    return torch.cuda.stream(stream), stream.cuda_stream      # makes its device current, too
+
+
+def _dense(t, name, shape, dtype, device):
+    """_need() with one test where it passes: these checks are half of a small call."""
+    if not (t is not None and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        _need(t, name, shape, dtype, device)
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_size(device_index, *query):
+    """gdr_linear_workspace_size on the (current) device, which it is a function of."""
+    return lib().gdr_linear_workspace_size(*query)
 
 
 def _strided(t, name, shape, dtype, device):
     """A [B,T,heads,d] input: unit stride along d; the other strides are the
-    library's to check."""
+    library's to check.  None for a dense one."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return None
     if t is None:
         raise ValueError(f"{name} is required")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.numel() and t.stride(-1) != 1:
+    if t.stride(-1) != 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
-    if t.numel() and any(n > 1 and s <= 0 for n, s in zip(t.shape[:3], t.stride()[:3])):
+    if any(n > 1 and s <= 0 for n, s in zip(t.shape[:3], t.stride()[:3])):
         raise ValueError(f"{name} must not be expanded along batch, tokens or heads")
     return _Stride3(*t.stride()[:3])
 
@@ -66,14 +82,17 @@ def _shape(q, k, v, log_decay, cu_seqlens):
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("inputs must be CUDA tensors (there is no CPU path)")
-    if q.dtype not in _DTYPES:
+    dtype = q.dtype
+    if dtype not in _DTYPES:
         raise ValueError("q, k, v must be bf16 or fp32")
     if H and (Hk == 0 or H % Hk):
         raise ValueError(f"v's {H} heads must be a multiple of the {Hk} heads of q and k")
-    sq = _strided(q, "q", (B, T, Hk, dk), q.dtype, dev)
-    sk = _strided(k, "k", (B, T, Hk, dk), q.dtype, dev)
-    sv = _strided(v, "v", (B, T, H, dv), q.dtype, dev)
-    _need(log_decay, "log_decay", (H,), torch.float32, dev)
+    a = LinearArgs(q=q.data_ptr(), k=k.data_ptr(), v=v.data_ptr(), log_decay=log_decay.data_ptr())
+    for t, name, shape in ((q, "q", q.shape), (k, "k", q.shape), (v, "v", (B, T, H, dv))):
+        stride = _strided(t, name, shape, dtype, dev)
+        if stride is not None:
+            setattr(a, name + "_stride", stride)
+    _dense(log_decay, "log_decay", (H,), torch.float32, dev)
     N = B
     if cu_seqlens is not None:
         if B != 1:
@@ -81,10 +100,9 @@ def _shape(q, k, v, log_decay, cu_seqlens):
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() == 0:
             raise ValueError("cu_seqlens must hold N + 1 offsets")
         N = cu_seqlens.numel() - 1
-        _need(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
-    a = LinearArgs(q=q.data_ptr(), k=k.data_ptr(), v=v.data_ptr(), q_stride=sq, k_stride=sk, v_stride=sv,
-                   log_decay=log_decay.data_ptr(), cu_seqlens=None if cu_seqlens is None else cu_seqlens.data_ptr())
-    return a, (_DTYPES[q.dtype], B, T, Hk, H, dk, dv, N)
+        _dense(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
+        a.cu_seqlens = cu_seqlens.data_ptr()
+    return a, (_DTYPES[dtype], B, T, Hk, H, dk, dv, N)
 
 
 def linear_forward(q, k, v, *, log_decay, initial_state=None, output_final_state=True, cu_seqlens=None,
@@ -109,7 +127,7 @@ def linear_forward(q, k, v, *, log_decay, initial_state=None, output_final_state
     dev, f32 = q.device, torch.float32
     pages = N
     if state_slots is not None:
-        _need(state_slots, "state_slots", (N,), torch.int32, dev)
+        _dense(state_slots, "state_slots", (N,), torch.int32, dev)
         pool = final_state if final_state is not None else initial_state
         if pool is None:
             raise ValueError("state_slots needs initial_state or final_state")
@@ -118,14 +136,14 @@ def linear_forward(q, k, v, *, log_decay, initial_state=None, output_final_state
         pages = pool.shape[0]
         a.state_slots, a.pages = state_slots.data_ptr(), pages
     if initial_state is not None:
-        _need(initial_state, "initial_state", (pages, H, dk, dv), f32, dev)
+        _dense(initial_state, "initial_state", (pages, H, dk, dv), f32, dev)
         a.initial_state = initial_state.data_ptr()
     if out is not None:
-        _need(out, "out", (B, T, H, dv), q.dtype, dev)
+        _dense(out, "out", (B, T, H, dv), q.dtype, dev)
     if final_state is not None:
-        _need(final_state, "final_state", (pages, H, dk, dv), f32, dev)
-    L = lib()
-    with _on(dev, stream) as handle:
+        _dense(final_state, "final_state", (pages, H, dk, dv), f32, dev)
+    where, handle = _on(dev, stream)
+    with where:
         if out is None:
             out = (torch.empty if cu_seqlens is None else torch.zeros)(B, T, H, dv, device=dev, dtype=q.dtype)
         if final_state is None and output_final_state:
@@ -133,9 +151,9 @@ def linear_forward(q, k, v, *, log_decay, initial_state=None, output_final_state
         a.o = out.data_ptr()
         if final_state is not None:
             a.final_state = final_state.data_ptr()
-        ws = L.gdr_linear_workspace_size(*dims, cu_seqlens is not None, 0)
+        ws = _workspace_size(dev.index, *dims, cu_seqlens is not None, 0)
         workspace = torch.empty(ws, device=dev, dtype=torch.uint8) if ws else None
-        check(L.gdr_linear_forward(*dims, ctypes.byref(a), float(scale), _ptr(workspace), ws, handle))
+        check(lib().gdr_linear_forward(*dims, a, scale, workspace.data_ptr() if ws else None, ws, handle))
     return out, final_state
 
 
@@ -151,25 +169,27 @@ def linear_backward(q, k, v, d_o, *, log_decay, initial_state=None, d_final_stat
     a, dims = _shape(q, k, v, log_decay, cu_seqlens)
     dt, B, T, Hk, H, dk, dv, N = dims
     dev, f32 = q.device, torch.float32
-    g = LinearGrads(d_o_stride=_strided(d_o, "d_o", (B, T, H, dv), q.dtype, dev))
-    g.d_o = d_o.data_ptr()
+    g = LinearGrads(d_o=d_o.data_ptr())
+    stride = _strided(d_o, "d_o", v.shape, q.dtype, dev)
+    if stride is not None:
+        g.d_o_stride = stride
     if initial_state is not None:
-        _need(initial_state, "initial_state", (N, H, dk, dv), f32, dev)
+        _dense(initial_state, "initial_state", (N, H, dk, dv), f32, dev)
         a.initial_state = initial_state.data_ptr()
     if d_final_state is not None:
-        _need(d_final_state, "d_final_state", (N, H, dk, dv), f32, dev)
+        _dense(d_final_state, "d_final_state", (N, H, dk, dv), f32, dev)
         g.d_final_state = d_final_state.data_ptr()
-    L = lib()
-    with _on(dev, stream) as handle:
+    where, handle = _on(dev, stream)
+    with where:
         new = torch.empty if cu_seqlens is None else torch.zeros
         grads = {"q": new(B, T, Hk, dk, device=dev, dtype=q.dtype), "k": new(B, T, Hk, dk, device=dev, dtype=q.dtype),
                  "v": new(B, T, H, dv, device=dev, dtype=q.dtype),
                  "initial_state": torch.empty(N, H, dk, dv, device=dev, dtype=f32)}
         g.dq, g.dk, g.dv = grads["q"].data_ptr(), grads["k"].data_ptr(), grads["v"].data_ptr()
         g.d_initial_state = grads["initial_state"].data_ptr()
-        ws = L.gdr_linear_workspace_size(*dims, cu_seqlens is not None, 1)
+        ws = _workspace_size(dev.index, *dims, cu_seqlens is not None, 1)
         workspace = torch.empty(ws, device=dev, dtype=torch.uint8) if ws else None
-        check(L.gdr_linear_backward(*dims, ctypes.byref(a), ctypes.byref(g), float(scale), _ptr(workspace), ws, handle))
+        check(lib().gdr_linear_backward(*dims, a, g, scale, workspace.data_ptr() if ws else None, ws, handle))
     return grads
 
 
@@ -191,23 +211,25 @@ def linear_decode_step(q, k, v, state, *, log_decay, state_slots=None, scale=1.0
         raise ValueError("q, k, v must be bf16 or fp32")
     if H and (Hk == 0 or H % Hk):
         raise ValueError(f"v's {H} heads must be a multiple of the {Hk} heads of q and k")
-    _need(q, "q", (N, Hk, dk), q.dtype, dev)
-    _need(k, "k", (N, Hk, dk), q.dtype, dev)
-    _need(v, "v", (N, H, dv), q.dtype, dev)
-    _need(log_decay, "log_decay", (H,), torch.float32, dev)
-    _need(state, "state", (pages, H, dk, dv), torch.float32, dev)
+    _dense(q, "q", (N, Hk, dk), q.dtype, dev)
+    _dense(k, "k", (N, Hk, dk), q.dtype, dev)
+    _dense(v, "v", (N, H, dv), q.dtype, dev)
+    _dense(log_decay, "log_decay", (H,), torch.float32, dev)
+    _dense(state, "state", (pages, H, dk, dv), torch.float32, dev)
     if state_slots is not None:
-        _need(state_slots, "state_slots", (N,), torch.int32, dev)
+        _dense(state_slots, "state_slots", (N,), torch.int32, dev)
     elif pages != N:
         raise ValueError(f"without state_slots state must hold one page per row ({N}), got {pages}")
     if out is not None:
-        _need(out, "out", (N, H, dv), q.dtype, dev)
-    with _on(dev, stream) as handle:
+        _dense(out, "out", (N, H, dv), q.dtype, dev)
+    where, handle = _on(dev, stream)
+    with where:
         if out is None:
             out = torch.empty(N, H, dv, device=dev, dtype=q.dtype)
-        check(lib().gdr_linear_decode_step(_DTYPES[q.dtype], N, Hk, H, dk, dv, _ptr(q), _ptr(k), _ptr(v),
-                                           _ptr(log_decay), _ptr(state), pages, _ptr(state_slots), _ptr(out),
-                                           float(scale), handle))
+        check(lib().gdr_linear_decode_step(_DTYPES[q.dtype], N, Hk, H, dk, dv, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                           log_decay.data_ptr(), state.data_ptr(), pages,
+                                           None if state_slots is None else state_slots.data_ptr(), out.data_ptr(), scale,
+                                           handle))
     return out
 
 
@@ -220,17 +242,18 @@ def copy_states(pool, src, dst, *, stream=None):
         raise ValueError("pool must be [pages,H,dk,dv] or [layers,pages,H,dk,dv]")
     if pool.device.type != "cuda":
         raise ValueError("pool must be a CUDA tensor (there is no CPU path)")
-    _need(pool, "pool", pool.shape, torch.float32, pool.device)
+    _dense(pool, "pool", pool.shape, torch.float32, pool.device)
     n = len(src)
     if len(dst) != n:
         raise ValueError(f"src has {n} pages and dst {len(dst)}")
     layers = pool.shape[0] if pool.dim() == 5 else 1
     pages, H, dk, dv = pool.shape[-4:]
-    if any(not -1 <= x < pages for x in src) or any(not 0 <= x < pages for x in dst):
+    if n and not (-1 <= min(src) and max(src) < pages and 0 <= min(dst) and max(dst) < pages):
         raise ValueError(f"pages must lie in [0, {pages}) (src: or be -1)")
     ints = ctypes.c_int * n
-    with _on(pool.device, stream) as handle:
-        check(lib().gdr_copy_states(_ptr(pool), layers, pages, H, dk, dv, ints(*src), ints(*dst), n, handle))
+    where, handle = _on(pool.device, stream)
+    with where:
+        check(lib().gdr_copy_states(pool.data_ptr(), layers, pages, H, dk, dv, ints(*src), ints(*dst), n, handle))
 
 
 class StateCache:
