@@ -294,6 +294,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int xh = blockIdx.x / sel.n;
   const int h = xh % p.H, x = xh / p.H;
   const LinRun &r = p.run[ri];
+  if (warp == W_COPY && lane < 3) prefetch_tmap(&maps.m[lane == 0 ? r.ib : lane == 1 ? r.ic : r.ia]);
   const bool rev = r.reverse != 0;
   const LinItem it = lin_item(p, x);
   const bool last = rev ? it.g == 0 : it.g == it.nseg - 1;   // in the run's order
@@ -313,7 +314,32 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tmem_alloc(reinterpret_cast<uint32_t *>(sm + M::SLOT), TMEM_COLS);
     tmem_relinquish();
   }
-  if (tid == 32) {
+  const int beg = it.g * p.seg, end = min(it.len, beg + p.seg);
+  const int nch = __shfl_sync(0xffffffffu, (end - beg + C - 1) / C, 0);
+  // copies of one chunk into its stage, and of the chunk that comes there next as far as L2
+  const int row_first = it.t0 + beg + (rev ? C * (nch - 1) : 0), row_step = rev ? -C : C;
+  auto copy_chunk = [&](int i, uint32_t at) {
+    const CUtensorMap *ma = &maps.m[r.ia], *mb = &maps.m[r.ib], *mc = &maps.m[r.ic];
+    const int ha = h / p.t[r.ia].div, hb = h / p.t[r.ib].div, hc = h / p.t[r.ic].div;
+    constexpr uint32_t bytes = (PHASE1 ? 0 : DA * 128) + DA * 128 + DC * 128;
+    const uint32_t bar = base + M::LOAD + 8 * at, dst = base + M::STAGE * at;
+    const int row = row_first + i * row_step;
+    expect_at(bar, bytes);
+    for (int d = 0; d < DA / 64; ++d) {
+      load_box(dst + M::B + 8192 * d, mb, bar, 64 * d, hb, row, it.b);
+      if (!PHASE1) load_box(dst + M::A + 8192 * d, ma, bar, 64 * d, ha, row, it.b);
+    }
+    for (int d = 0; d < DC / 64; ++d) load_box(dst + M::CT + 8192 * d, mc, bar, 64 * d, hc, row, it.b);
+    if (i + NST < nch) {
+      const int ahead = row + NST * row_step;
+      for (int d = 0; d < DA / 64; ++d) {
+        tma_prefetch_4d(mb, 64 * d, hb, ahead, it.b);
+        if (!PHASE1) tma_prefetch_4d(ma, 64 * d, ha, ahead, it.b);
+      }
+      for (int d = 0; d < DC / 64; ++d) tma_prefetch_4d(mc, 64 * d, hc, ahead, it.b);
+    }
+  };
+  if (tid == 32 * W_COPY) {
     auto init = [&](uint32_t at, int n, uint32_t count) {
       for (int i = 0; i < n; ++i) mbar_init(reinterpret_cast<uint64_t *>(sm + at + 8 * i), count);
     };
@@ -332,6 +358,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     init(M::PTAIL, 1, 1);
     *reinterpret_cast<uint32_t *>(sm + M::ABORT) = 0;
     fence_mbar_init();
+    // the first chunks: their tensors are inputs of the call, whatever grid this one depends on
+    for (int i = 0; i < NST && i < nch; ++i) copy_chunk(i, i);
   }
   if (tid >= 64 && tid < 64 + 65) {
     const int m = tid - 64;
@@ -351,8 +379,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const uint32_t tmem = *reinterpret_cast<uint32_t *>(sm + M::SLOT);   // 0: the CTA holds all of tensor memory (the MMA warp writes it so)
   griddep_launch_dependents();
 
-  const int beg = it.g * p.seg, end = min(it.len, beg + p.seg);
-  const int nch = __shfl_sync(0xffffffffu, (end - beg + C - 1) / C, 0);
   const int page = lin_page(p, it.n);
   // (the chain kernel has written the end state of a sequence with several segments)
   float *const final_page = !PHASE1 && it.nseg == 1 && r.s_final && page >= 0
@@ -365,29 +391,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (warp == W_COPY) {
     // ---------------------------------------------------------------- copies
     if (lane == 0) {
-      const CUtensorMap *ma = &maps.m[r.ia], *mb = &maps.m[r.ib], *mc = &maps.m[r.ic];
-      const int ha = h / p.t[r.ia].div, hb = h / p.t[r.ib].div, hc = h / p.t[r.ic].div;
-      constexpr uint32_t bytes = (PHASE1 ? 0 : DA * 128) + DA * 128 + DC * 128;
-      const int step = rev ? -C : C;
-      int row = it.t0 + beg + (rev ? C * (nch - 1) : 0), i = 0;
+      int i = min(nch, NST);   // the first ones are under way
       Ring<NST> st;
-      for (; i < nch; ++i, st.next(), row += step) {
-        const uint32_t bar = base + M::LOAD + 8 * st.at, dst = base + M::STAGE * st.at;
-        if (i >= NST && !wait_at(base + M::FREE + 8 * st.at, st.phase ^ 1, abort)) break;
-        expect_at(bar, bytes);
-        for (int d = 0; d < DA / 64; ++d) {
-          load_box(dst + M::B + 8192 * d, mb, bar, 64 * d, hb, row, it.b);
-          if (!PHASE1) load_box(dst + M::A + 8192 * d, ma, bar, 64 * d, ha, row, it.b);
-        }
-        for (int d = 0; d < DC / 64; ++d) load_box(dst + M::CT + 8192 * d, mc, bar, 64 * d, hc, row, it.b);
-        if (i + NST < nch) {   // and the chunk that comes into this stage next, as far as L2
-          const int ahead = row + NST * step;
-          for (int d = 0; d < DA / 64; ++d) {
-            tma_prefetch_4d(mb, 64 * d, hb, ahead, it.b);
-            if (!PHASE1) tma_prefetch_4d(ma, 64 * d, ha, ahead, it.b);
-          }
-          for (int d = 0; d < DC / 64; ++d) tma_prefetch_4d(mc, 64 * d, hc, ahead, it.b);
-        }
+      for (; i < nch; ++i, st.next()) {
+        if (!wait_at(base + M::FREE + 8 * st.at, st.phase, abort)) break;
+        copy_chunk(i, st.at);
       }
       // nothing may land in shared memory after the CTA (each wait bounded)
       for (int j = i > NST ? i - NST : 0; j < i; ++j)
