@@ -18,29 +18,28 @@ constexpr int kChainThreads = 256;
 
 __global__ void __launch_bounds__(kChainThreads) linear_chain_kernel(const LinProblem p) {
   tc::griddep_launch_dependents();
-  const int h = blockIdx.y % p.H;
-  const LinRun &r = p.run[blockIdx.y / p.H];
+  const LinRun &r = p.run[blockIdx.z];
   const int e4 = blockIdx.x * kChainThreads + threadIdx.x;   // float4 of the state
   tc::griddep_wait();
-  const float ld = __ldg(p.log_decay + h);
-  const float full = static_cast<float>(exp(static_cast<double>(ld) * p.seg));
-  const size_t page_elems = static_cast<size_t>(r.da) * r.dc;
-  if (static_cast<size_t>(e4) * 4 >= page_elems) return;
-  for (int n = blockIdx.z; n < p.N; n += gridDim.z) {
-    int t0 = 0, len = p.T, x0 = n * p.G;
+  const size_t page_vec = static_cast<size_t>(r.da) * r.dc / 4;
+  if (e4 >= static_cast<int>(page_vec)) return;
+  for (int u = blockIdx.y; u < p.N * p.H; u += gridDim.y) {
+    const int n = u / p.H, h = u - n * p.H;
+    int len = p.T, x = n * p.G, nseg = p.G;
     if (p.cu) {
-      t0 = lin_cu(p, n);
+      const int t0 = lin_cu(p, n);
       len = max(lin_cu(p, n + 1) - t0, 0);
-      x0 = t0 / p.seg + n;
+      x = t0 / p.seg + n;
+      nseg = max(1, (len + p.seg - 1) / p.seg);
     }
-    const int nseg = max(1, (len + p.seg - 1) / p.seg);
     if (nseg == 1) continue;
     const int tail = len - (nseg - 1) * p.seg;   // tokens of the last segment
-    const float ftail = tail == p.seg ? full : static_cast<float>(exp(static_cast<double>(ld) * tail));
+    const float ld = __ldg(p.log_decay + h);
+    const float full = lin_pow64(ld, p.seg), ftail = tail == p.seg ? full : lin_pow64(ld, tail);
     const int page = lin_page(p, n);
     float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r.s0 && page >= 0) {
-      const float *src = r.s0 + (static_cast<size_t>(page) * p.H + h) * page_elems;
+      const float *src = r.s0 + (static_cast<size_t>(page) * p.H + h) * page_vec * 4;
       if (r.s0_t) {
         const int row = e4 * 4 / r.dc, col = e4 * 4 % r.dc;
         cur = make_float4(src[(col + 0) * r.da + row], src[(col + 1) * r.da + row], src[(col + 2) * r.da + row],
@@ -49,27 +48,27 @@ __global__ void __launch_bounds__(kChainThreads) linear_chain_kernel(const LinPr
         cur = *reinterpret_cast<const float4 *>(src + 4 * e4);
       }
     }
-    const size_t step = static_cast<size_t>(p.H) * page_elems / 4;
-    float4 *X = reinterpret_cast<float4 *>(r.X) + (static_cast<size_t>(x0) * p.H + h) * (page_elems / 4) + e4;
-    float4 *fin = r.s_final && page >= 0 ? reinterpret_cast<float4 *>(
-        r.s_final + (static_cast<size_t>(page) * p.H + h) * page_elems) + e4 : nullptr;
+    float4 *X = reinterpret_cast<float4 *>(r.X) + (static_cast<size_t>(x) * p.H + h) * page_vec + e4;
+    const size_t xs = p.H * page_vec;
+    float4 *fin = r.s_final && page >= 0
+                      ? reinterpret_cast<float4 *>(r.s_final) + (static_cast<size_t>(page) * p.H + h) * page_vec + e4 : nullptr;
     constexpr int U = 8;
     for (int i0 = 0; i0 < nseg; i0 += U) {
       float4 d[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i0 + u < nseg - (fin ? 0 : 1)) d[u] = X[(r.reverse ? nseg - 1 - (i0 + u) : i0 + u) * step];
+      for (int k = 0; k < U; ++k)
+        if (i0 + k < nseg - (fin ? 0 : 1)) d[k] = X[(r.reverse ? nseg - 1 - (i0 + k) : i0 + k) * xs];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u;
+      for (int k = 0; k < U; ++k) {
+        const int i = i0 + k;
         if (i >= nseg) break;
-        X[(r.reverse ? nseg - 1 - i : i) * step] = cur;
+        X[(r.reverse ? nseg - 1 - i : i) * xs] = cur;
         if (i == nseg - 1 && !fin) break;
         const float f = i == (r.reverse ? 0 : nseg - 1) ? ftail : full;   // the sequence's last segment may be short
-        cur.x = fmaf(f, cur.x, d[u].x);
-        cur.y = fmaf(f, cur.y, d[u].y);
-        cur.z = fmaf(f, cur.z, d[u].z);
-        cur.w = fmaf(f, cur.w, d[u].w);
+        cur.x = fmaf(f, cur.x, d[k].x);
+        cur.y = fmaf(f, cur.y, d[k].y);
+        cur.z = fmaf(f, cur.z, d[k].z);
+        cur.w = fmaf(f, cur.w, d[k].w);
       }
     }
     if (fin) *fin = cur;
@@ -108,7 +107,8 @@ cudaError_t gdr_launch_linear_chain(const gdr::LinProblem &p, bool pdl, cudaStre
   using namespace gdr;
   const int elems = p.run[0].da * p.run[0].dc;   // the same for every run of a call
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((elems / 4 + kChainThreads - 1) / kChainThreads, p.H * p.nrun, p.N < 65535 ? p.N : 65535);
+  const long pairs = static_cast<long>(p.N) * p.H;
+  cfg.gridDim = dim3((elems / 4 + kChainThreads - 1) / kChainThreads, static_cast<unsigned>(pairs < 65535 ? pairs : 65535), p.nrun);
   cfg.blockDim = dim3(kChainThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -130,42 +130,69 @@ cudaError_t gdr_launch_linear_group_sum(const float *x, void *y, bool bf16, int 
   return cudaGetLastError();
 }
 
+// bf16, a dense batch: one CTA per SM and (run, segment, head).  Times in us on a B200 with
+// its clock under load: a round of CTAs costs kStart, and a chunk of 64 tokens kChunk2 with
+// outputs, kChunk1 in phase 1; less where half of the SMs stay idle, whose power the others get.
+// (64 sequences of 32 chunks: whole 59 us, in two segments each 61, in four 98; 192 runs of 32
+// chunks whole 114, in two 160; 16 of 1024 in nine segments 390, in five 400, in 27 416.)
+namespace {
+constexpr float kStart = 5.f, kChunk1 = 1.15f, kChunk2 = 2.1f, kChunk2Half = 1.75f, kSelfChain = 1.5f, kChainKernel = 8.f;
+
+int plan_dense(const gdr::LinProblem &p, int sms) {   // segments per sequence
+  const long units = static_cast<long>(p.N) * p.H * p.nrun;
+  const int nc = (p.T + 63) / 64;
+  float best = 0.f;
+  int G = 1;
+  for (int g = 1; g <= 64 && (g == 1 || 2 * g <= nc); ++g) {
+    const int len = (nc + g - 1) / g;
+    const long rounds = (units * g + sms - 1) / sms;
+    const float chunk2 = 2 * units * g <= sms ? kChunk2Half : kChunk2;
+    float t = rounds * (kStart + len * chunk2);
+    if (g > 1) t += rounds * (kStart + len * kChunk1) + (g <= gdr::kLinSelfChain ? kSelfChain * (g - 1) : kChainKernel);
+    if (g == 1 || t < best) {
+      best = t;
+      G = g;
+    }
+  }
+  return G;
+}
+}  // namespace
+
 void gdr_linear_plan(gdr::LinProblem *p, int sms) {
-  const long total = static_cast<long>(p->B) * p->T;
+  const long total = static_cast<long>(p->B) * p->T, units = static_cast<long>(p->N) * p->H * p->nrun;
   long seg;
   if (p->bf16_io) {
-    // One CTA per SM and (run, segment, head).
-    const long slots = sms, heads = static_cast<long>(p->H) * p->nrun;
     if (!p->cu) {
-      const long per_seq = slots / (heads * p->N > 0 ? heads * p->N : 1);   // segments per sequence that fit
-      seg = per_seq <= 1 ? p->T : (p->T + per_seq - 1) / per_seq;
+      const int nc = (p->T + 63) / 64, g = plan_dense(*p, sms);
+      seg = 64l * ((nc + g - 1) / g);
     } else {
-      seg = total * heads / slots;
+      // lengths unknown here: segments that give every SM one (a packed batch of 9200 tokens, 16 heads:
+      // 1024 tokens 83 us, 512: 95, 2048: 111)
+      seg = total * p->H * p->nrun / sms;
+      if (seg < 256) seg = 256;
     }
-    if (seg < 128) seg = 128;
+    seg = (seg + 63) / 64 * 64;
   } else {
-    // Token kernel: one warp per (run, segment, head, 8 columns), 12 or so resident
-    // per SM; segments of at least 64 tokens until the device is full.
-    long warps = 0;
-    for (int i = 0; i < p->nrun; ++i) warps += static_cast<long>(p->H) * (p->run[i].dc / 8);
-    const long slots = 12L * sms;
-    seg = (total * warps + slots - 1) / slots;        // tokens per segment that fill the slots
-    if (!p->cu && static_cast<long>(p->N) * warps >= slots) seg = p->T;
+    // token kernel: three CTAs or so per SM
+    seg = total * p->H * p->nrun / (3L * sms);
+    seg = (seg + 15) / 16 * 16;
+    if (seg < 32) seg = 32;
+    if (!p->cu && units >= 2L * sms) seg = p->T;
   }
-  seg = (seg + 63) / 64 * 64;
-  if (seg < 64) seg = 64;
-  const long whole = (p->T + 63) / 64 * 64;
-  if (seg > whole) seg = whole > 0 ? whole : 64;
+  if (seg > p->T) seg = p->T;
+  if (seg < 1) seg = 1;
   p->seg = static_cast<int>(seg);
   p->G = p->T > 0 ? (p->T + p->seg - 1) / p->seg : 1;
   p->items = p->cu ? p->T / p->seg + p->N : p->N * p->G;
 }
 
-// Segment states of all runs, when any sequence may have more than one segment.
+// Segment states of all runs, twice where phase 2 may chain them itself.
+static size_t run_floats(const gdr::LinProblem &p, int i) {
+  return gdr::lin_segmented(p) ? static_cast<size_t>(gdr::lin_blocks(p)) * p.run[i].da * p.run[i].dc : 0;
+}
 size_t gdr_linear_workspace_bytes(const gdr::LinProblem &p) {
-  if (p.T <= p.seg) return 0;
   size_t floats = 0;
-  for (int i = 0; i < p.nrun; ++i) floats += static_cast<size_t>(p.items) * p.H * p.run[i].da * p.run[i].dc;
+  for (int i = 0; i < p.nrun; ++i) floats += run_floats(p, i) * (p.G <= gdr::kLinSelfChain ? 2 : 1);
   return floats * sizeof(float);
 }
 
@@ -173,9 +200,12 @@ cudaError_t gdr_launch_linear(gdr::LinProblem &p, void *ws, cudaStream_t s, std:
   float *X = static_cast<float *>(ws);
   for (int i = 0; i < p.nrun; ++i) {
     p.run[i].X = X;
-    X += static_cast<size_t>(p.items) * p.H * p.run[i].da * p.run[i].dc;
+    X += run_floats(p, i);
+    if (p.G > gdr::kLinSelfChain) continue;
+    p.run[i].XS = X;
+    X += run_floats(p, i);
   }
-  const bool segmented = p.T > p.seg;
+  const bool segmented = gdr::lin_segmented(p);
   const bool chunk = p.bf16_io && p.T > 0;   // no tokens: the token kernel copies the states
   gdr::LinChunkMaps maps;
   if (chunk && !gdr_linear_chunk_maps(p, &maps)) return *err = "tensor map: ", cudaErrorInvalidValue;
@@ -183,9 +213,13 @@ cudaError_t gdr_launch_linear(gdr::LinProblem &p, void *ws, cudaStream_t s, std:
     return chunk ? gdr_launch_linear_chunk(p, maps, phase1, pdl, s) : gdr_launch_linear_token(p, phase1, pdl, s);
   };
   cudaError_t e;
+  // (an end state in the place of its start state is written by the chain kernel: phase 2's segments
+  // read the start state side by side)
+  p.chained = segmented && p.G > gdr::kLinSelfChain;
+  for (int i = 0; i < p.nrun; ++i) p.chained |= segmented && p.run[i].s0 && p.run[i].s0 == p.run[i].s_final;
   if (segmented) {
     if ((e = phase(true, false)) != cudaSuccess) return *err = "segment states: ", e;
-    if ((e = gdr_launch_linear_chain(p, true, s)) != cudaSuccess) return *err = "segment chain: ", e;
+    if (p.chained && (e = gdr_launch_linear_chain(p, true, s)) != cudaSuccess) return *err = "segment chain: ", e;
   }
   if ((e = phase(false, segmented)) != cudaSuccess) return *err = "runs: ", e;
   return cudaSuccess;

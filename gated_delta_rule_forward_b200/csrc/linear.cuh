@@ -16,8 +16,9 @@
 // initial state, and its start is the gradient of the final state.
 //
 // Long sequences are cut into segments of `seg` tokens that run side by side:
-// phase 1 leaves every segment's end state from a zero start, a chain kernel
-// turns those into start states, and phase 2 runs all segments from them.
+// phase 1 leaves every segment's end state from a zero start, those are chained
+// into start states (by each segment of phase 2 for itself where there are few,
+// by a kernel in between otherwise), and phase 2 runs all segments from them.
 #pragma once
 
 #include <string>
@@ -45,7 +46,8 @@ struct LinRun {
   const float *s0;      // start state [.., H, da, dc], or null (zeros)
   int s0_t;             // s0 is laid out [.., H, dc, da]
   float *s_final;       // end state [.., H, da, dc], or null
-  float *X;             // [items, H, da, dc] segment states, used when segmented
+  float *X;             // segment states [slots, da, dc], used when segmented
+  float *XS;            // and the start states that phase 2 makes of them
 };
 
 struct LinProblem {
@@ -58,34 +60,50 @@ struct LinProblem {
   const int *slots;      // [N] page of each sequence's state, or null (page n)
   int pages;
   const float *log_decay;   // [H]
-  int seg;               // tokens per segment (a multiple of 64)
-  int G;                 // dense: segments per sequence
-  int items;             // (sequence, segment) pairs, an upper bound when packed
+  int seg;               // tokens per segment
+  int G;                 // segments of a sequence (packed: at most)
+  int items;             // (sequence, segment) pairs (packed: an upper bound)
+  int chained;           // X holds start states already (the chain kernel ran)
 };
 
+// A run's blocks are its segments of every head; each has a state in X.
+inline long lin_blocks(const LinProblem &p) { return static_cast<long>(p.items) * p.H; }
+inline bool lin_segmented(const LinProblem &p) { return p.G > 1; }
+// Segments up to which phase 2 chains the states itself.
+constexpr int kLinSelfChain = 4;
+
 #ifdef __CUDACC__
-// One (sequence, segment).  `ok` is false for an index past the last segment.
+// One segment of one (sequence, head).  `ok` is false for an index past the last one.
 struct LinItem {
   bool ok;
-  int n, g, nseg, b;
+  int n, h, g, nseg, b;
   int t0, len;   // the sequence's first token within its batch row, its length
+  int beg, end;  // the segment's tokens within the sequence
+  int slot, step;   // its entry of X, and the distance to the next segment's
 };
 
 __device__ __forceinline__ int lin_cu(const LinProblem &p, int n) { return min(max(__ldg(p.cu + n), 0), p.T); }
 
-// Sequence n's items start at cu[n] / seg + n: consecutive starts differ by at
+// Packed: sequence n's items start at cu[n] / seg + n: consecutive starts differ by at
 // least the sequence's segments (and by at least one for an empty sequence), so
 // a packed batch needs no table.  The search is 32-ary, one probe per lane;
 // offsets are clamped to [0, T], so that any cu_seqlens stays within the rows.
-__device__ __forceinline__ LinItem lin_item(const LinProblem &p, int x) {
+__device__ __forceinline__ LinItem lin_item(const LinProblem &p, int block) {
   LinItem it;
+  // neighbouring heads in neighbouring blocks: they read neighbouring rows
+  const int x = block / p.H;
+  it.h = block - x * p.H;
+  it.slot = block;
+  it.step = p.H;
   if (!p.cu) {
     it.n = x / p.G;
     it.g = x - it.n * p.G;
+    it.nseg = p.G;
     it.b = it.n;
     it.t0 = 0;
     it.len = p.T;
-    it.nseg = p.G;
+    it.beg = it.g * p.seg;
+    it.end = min(p.T, it.beg + p.seg);
     it.ok = true;
     return it;
   }
@@ -113,7 +131,14 @@ __device__ __forceinline__ LinItem lin_item(const LinProblem &p, int x) {
   it.nseg = max(1, (it.len + p.seg - 1) / p.seg);
   it.g = x - (it.t0 / p.seg + lo);
   it.ok = found && it.g < it.nseg;
+  it.beg = it.g * p.seg;
+  it.end = min(it.len, it.beg + p.seg);
   return it;
+}
+
+// lambda^n by way of 64 bits.
+__device__ __forceinline__ float lin_pow64(float log_decay, int n) {
+  return static_cast<float>(exp(static_cast<double>(log_decay) * n));
 }
 
 // Page of sequence n's state, or -1 where its slot lies outside the pool.
@@ -121,6 +146,52 @@ __device__ __forceinline__ int lin_page(const LinProblem &p, int n) {
   if (!p.slots) return n;
   const int s = __ldg(p.slots + n);
   return s >= 0 && s < p.pages ? s : -1;
+}
+
+// A segment's start state from the start state of its sequence and the end states (from
+// zero) of the segments before it in the run's order, and after the last segment the
+// end state of the sequence where it is wanted.  The whole block; `to` may be read by it after a
+// barrier.
+__device__ __forceinline__ void lin_self_chain(const LinProblem &p, const LinRun &r, const LinItem &it, int page,
+                                               bool last, int da, int dc, float *to, int tid, int threads) {
+  const float ld = __ldg(p.log_decay + it.h);
+  const size_t elems = static_cast<size_t>(da) * dc;
+  const float *X = r.X + static_cast<size_t>(it.slot - it.g * it.step) * elems;   // segment 0's
+  const int before = r.reverse ? it.nseg - 1 - it.g : it.g;
+  const bool fin = last && r.s_final && page >= 0;
+  const size_t at_page = (static_cast<size_t>(page < 0 ? 0 : page) * p.H + it.h) * elems;
+  float f[kLinSelfChain];
+#pragma unroll
+  for (int k = 0; k < kLinSelfChain; ++k) {   // the run's k-th segment
+    const int seg = r.reverse ? it.nseg - 1 - k : k;
+    f[k] = k < before + fin ? lin_pow64(ld, min(it.len, (seg + 1) * p.seg) - seg * p.seg) : 0.f;
+  }
+  for (int e = 4 * tid; e < static_cast<int>(elems); e += 4 * threads) {
+    float4 d[kLinSelfChain];
+#pragma unroll
+    for (int k = 0; k < kLinSelfChain; ++k) {
+      const int seg = r.reverse ? it.nseg - 1 - k : k;
+      if (k < before + fin) d[k] = *reinterpret_cast<const float4 *>(X + static_cast<size_t>(seg) * it.step * elems + e);
+    }
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r.s0 && page >= 0) {
+      const float *src = r.s0 + at_page;
+      const int row = e / dc, col = e - row * dc;
+      if (r.s0_t) s = make_float4(src[(col + 0) * da + row], src[(col + 1) * da + row], src[(col + 2) * da + row],
+                                  src[(col + 3) * da + row]);
+      else s = *reinterpret_cast<const float4 *>(src + e);
+    }
+#pragma unroll
+    for (int k = 0; k < kLinSelfChain; ++k) {
+      if (k == before) *reinterpret_cast<float4 *>(to + e) = s;
+      if (k >= before + fin) continue;
+      s.x = fmaf(f[k], s.x, d[k].x);
+      s.y = fmaf(f[k], s.y, d[k].y);
+      s.z = fmaf(f[k], s.z, d[k].z);
+      s.w = fmaf(f[k], s.w, d[k].w);
+    }
+    if (fin) *reinterpret_cast<float4 *>(r.s_final + at_page + e) = s;
+  }
 }
 
 // exp(n * log_decay), the product's rounding error carried into the result;
@@ -136,9 +207,9 @@ __device__ __forceinline__ float lin_pow(float log_decay, int n) {
 
 }  // namespace gdr
 
-// Launchers.  `phase1`: end states of all segments but each sequence's last
-// (in the run's order) from zero, into X; otherwise the whole runs, segments
-// starting from X where a sequence has more than one.
+// Launchers.  `phase1`: end states of the segments from zero, into X (of a
+// sequence's last one, in the run's order, only where its end state is wanted);
+// otherwise the runs themselves.
 cudaError_t gdr_launch_linear_token(const gdr::LinProblem &p, bool phase1, bool pdl, cudaStream_t s);
 cudaError_t gdr_launch_linear_chain(const gdr::LinProblem &p, bool pdl, cudaStream_t s);
 

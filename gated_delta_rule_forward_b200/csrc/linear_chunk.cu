@@ -291,12 +291,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform in the compiler's eyes, and so the branches on it
   const int ri = sel.run[blockIdx.x % sel.n];
-  const int xh = blockIdx.x / sel.n;
-  const int h = xh % p.H, x = xh / p.H;
   const LinRun &r = p.run[ri];
   if (warp == W_COPY && lane < 3) prefetch_tmap(&maps.m[lane == 0 ? r.ib : lane == 1 ? r.ic : r.ia]);
   const bool rev = r.reverse != 0;
-  const LinItem it = lin_item(p, x);
+  const LinItem it = lin_item(p, blockIdx.x / sel.n);
+  const int h = it.h;
   const bool last = rev ? it.g == 0 : it.g == it.nseg - 1;   // in the run's order
   if (!it.ok || (PHASE1 && last && (it.nseg == 1 || !r.s_final))) {
     griddep_launch_dependents();
@@ -314,7 +313,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tmem_alloc(reinterpret_cast<uint32_t *>(sm + M::SLOT), TMEM_COLS);
     tmem_relinquish();
   }
-  const int beg = it.g * p.seg, end = min(it.len, beg + p.seg);
+  const int beg = it.beg, end = it.end;
   const int nch = __shfl_sync(0xffffffffu, (end - beg + C - 1) / C, 0);
   // copies of one chunk into its stage, and of the chunk that comes there next as far as L2
   const int row_first = it.t0 + beg + (rev ? C * (nch - 1) : 0), row_step = rev ? -C : C;
@@ -380,12 +379,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   griddep_launch_dependents();
 
   const int page = lin_page(p, it.n);
-  // (the chain kernel has written the end state of a sequence with several segments)
+  // (the end state of a sequence with several segments is made from phase 1's)
   float *const final_page = !PHASE1 && it.nseg == 1 && r.s_final && page >= 0
                                 ? r.s_final + (static_cast<size_t>(page) * p.H + h) * DA * DC : nullptr;
   // a state that leaves in fp32 takes all three terms; one that only makes bf16 outputs, two
   const bool three = PHASE1 || __shfl_sync(0xffffffffu, final_page != nullptr, 0);
   const int tail_i = rev ? 0 : nch - 1, tail_n = end - beg - C * (nch - 1);   // the only chunk that may be short
+
+  // The grid before: phase 1's states, or the chain kernel's.  (A sequence that runs whole
+  // needs nothing of it, and may run beside it.)
+  const float *start = r.X + static_cast<size_t>(it.slot) * DA * DC;
+  if (PHASE1 || it.nseg > 1) griddep_wait();
+  if (!PHASE1 && it.nseg > 1 && !p.chained) {
+    float *mine = r.XS + static_cast<size_t>(it.slot) * DA * DC;
+    lin_self_chain(p, r, it, page, last, DA, DC, mine, tid, NTHREADS);
+    start = mine;
+    __syncthreads();
+  }
 
   if (warp >= W_COPY) regs_dec<R_CTL>();
   if (warp == W_COPY) {
@@ -610,7 +620,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int tp = 16 * quad + (lane & 15), cp = 4 * half + (lane >> 4);
     const uint32_t pput0 = base + M::P + sw128(tp, cp), pput1 = base + M::P + sw128(tp, cp + 2);
     const uint32_t plane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + T::P + 32 * half;
-    griddep_wait();
     Ring<2> bf, obf;   // of P's chunk, and of the output's, one behind
     for (int i = 0; !PHASE1 && i <= nch; ++i, bf.next()) {
       if (i < nch) {   // P of chunk i, with its decays
@@ -721,10 +730,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     uint64_t S[SN / 2];
 #pragma unroll
     for (int j = 0; j < SN / 2; ++j) S[j] = 0;
-    griddep_wait();   // the chain kernel's start states
     if (!PHASE1 && has_c) {
       if (it.nseg > 1) {
-        const float *src = r.X + ((static_cast<size_t>(x) * p.H + h) * DA + da0) * DC + dcr;
+        const float *src = start + static_cast<size_t>(da0) * DC + dcr;
 #pragma unroll
         for (int j = 0; j < SN / 2; ++j) S[j] = pair_f32(src[2 * j * DC], src[(2 * j + 1) * DC]);
       } else if (r.s0 && page >= 0) {
@@ -794,7 +802,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       tc_fence_after();
       store_operand();
     }
-    float *dst = PHASE1 ? r.X + (static_cast<size_t>(x) * p.H + h) * DA * DC : final_page;
+    float *dst = PHASE1 ? r.X + static_cast<size_t>(it.slot) * DA * DC : final_page;
     if (dst && has_c && ok) {
       dst += da0 * DC + dcr;
 #pragma unroll
@@ -830,7 +838,7 @@ cudaError_t launch(const LinProblem &p, const LinChunkMaps &maps, const LinRunSe
     set.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long>(p.items) * p.H * sel.n));
+  cfg.gridDim = dim3(static_cast<unsigned>(lin_blocks(p) * sel.n));
   cfg.blockDim = dim3(NTHREADS);
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
