@@ -133,10 +133,10 @@ cudaError_t gdr_launch_linear_group_sum(const float *x, void *y, bool bf16, int 
 // bf16, a dense batch: one CTA per SM and (run, segment, head).  Times in us on a B200 with
 // its clock under load: a round of CTAs costs kStart, and a chunk of 64 tokens kChunk2 with
 // outputs, kChunk1 in phase 1; less where half of the SMs stay idle, whose power the others get.
-// (64 sequences of 32 chunks: whole 59 us, in two segments each 61, in four 98; 192 runs of 32
-// chunks whole 114, in two 160; 16 of 1024 in nine segments 390, in five 400, in 27 416.)
+// (64 sequences of 32 chunks: whole 66 us, in two segments each 58, in four 74; 192 runs of 32
+// chunks whole 110, in two 139; 16 of 1024 in nine segments 345, in eight 348, in 18 349, in four 491.)
 namespace {
-constexpr float kStart = 5.f, kChunk1 = 1.15f, kChunk2 = 2.1f, kChunk2Half = 1.75f, kSelfChain = 1.5f, kChainKernel = 8.f;
+constexpr float kStart = 5.f, kChunk1 = 1.15f, kChunk2 = 2.1f, kChunk2Half = 1.9f, kSelfChain = 1.5f, kChainKernel = 8.f;
 
 int plan_dense(const gdr::LinProblem &p, int sms) {   // segments per sequence
   const long units = static_cast<long>(p.N) * p.H * p.nrun;
