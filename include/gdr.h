@@ -297,7 +297,9 @@ gdr_status_t gdr_backward(int variant, int dtype, int B, int T, int H, int dk, i
  *    of Hk, and value head h reads key head h / (H / Hk);
  *  - q, k and v (and the backward's d_o) may be strided: unit stride along d,
  *    and batch, token and head strides that are multiples of 16 bytes; three
- *    zero strides mean a dense tensor.  Outputs and states are dense;
+ *    zero strides mean a dense tensor.  Outputs and states are dense, and an
+ *    output overlaps no input and no other output (final_state may be
+ *    initial_state);
  *  - a packed batch: cu_seqlens (device, int32, N + 1 non-decreasing offsets
  *    from 0 to at most T) cuts the T tokens of one row (B = 1) into N
  *    sequences, which may be empty; rows behind the last sequence are not

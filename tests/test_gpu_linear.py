@@ -415,3 +415,118 @@ def test_empty_calls():
     assert gdr.linear_decode_step(e(0, 2, 64), e(0, 2, 64), e(0, 2, 64), e(3, 2, 64, 64, dt=F32), log_decay=ld,
                                   state_slots=e(0, dt=torch.int32)).shape == (0, 2, 64)
     fine()
+
+
+# (the number of segments that the plan takes on 148 SMs: 2, 3, 4, 4, more than 4)
+@pytest.mark.parametrize("dtype,T,Hk,H,dk,dv", [(BF16, 2048, 25, 50, 64, 64), (BF16, 1400, 18, 36, 64, 64),
+                                               (BF16, 901, 1, 2, 128, 128), (BF16, 705, 2, 4, 64, 128),
+                                               (BF16, 1700, 1, 3, 128, 64), (F32, 901, 1, 2, 128, 128)])
+def test_segments(dtype, T, Hk, H, dk, dv):
+    """Segments chained by themselves and by the kernel between: decays that forget and that do not, shared heads,
+    states both ways, the end state in the place of the start state."""
+    q, k, v, g = tensors(T + 3, 1, T, Hk, H, dk, dv, dtype)
+    S0 = randn(g, 1, H, dk, dv)
+    ld = decays(H, T)
+    o, S = gdr.linear_forward(q, k, v, log_decay=ld, initial_state=S0, scale=0.1)
+    state = S0.clone()
+    o2, S2 = gdr.linear_forward(q, k, v, log_decay=ld, initial_state=state, final_state=state, scale=0.1)
+    o3, none = gdr.linear_forward(q, k, v, log_decay=ld, initial_state=S0, output_final_state=False, scale=0.1)
+    fine()
+    assert none is None and torch.equal(o, o3) and S2.data_ptr() == state.data_ptr()
+    ref.check_forward(q[0], k[0], v[0], ld, S0[0], 0.1, o[0], S[0])
+    ref.check_forward(q[0], k[0], v[0], ld, S0[0], 0.1, o2[0], S2[0], "in place")
+
+
+@pytest.mark.parametrize("dtype,T,Hk,H,dk,dv,state", [(BF16, 2048, 6, 18, 64, 64, True), (BF16, 901, 1, 2, 128, 64, True),
+                                                     (BF16, 1100, 3, 3, 64, 128, False), (F32, 500, 1, 2, 64, 128, True)])
+def test_backward_segments(dtype, T, Hk, H, dk, dv, state):
+    q, k, v, g = tensors(T + 4, 1, T, Hk, H, dk, dv, dtype)
+    do = randn(g, 1, T, H, dv, dtype=dtype)
+    S0, dS = (randn(g, 1, H, dk, dv), randn(g, 1, H, dk, dv)) if state else (None, None)
+    ld = decays(H, T)
+    x = gdr.linear_backward(q, k, v, do, log_decay=ld, initial_state=S0, d_final_state=dS, scale=0.3)
+    fine()
+    ref.check_grads(q[0], k[0], v[0], do[0], ld, S0[0] if state else None, dS[0] if state else None, 0.3,
+                    (x["q"][0], x["k"][0], x["v"][0], x["initial_state"][0]))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_many_short_sequences(dtype):
+    N, H, d = 2000, 1, 64
+    rng = random.Random(1)
+    lens = [rng.choice([0, 0, 1, 1, 2, 3]) for _ in range(N)]
+    T = sum(lens)
+    q, k, v, g = tensors(31, 1, T, H, H, d, d, dtype)
+    S0 = randn(g, N, H, d, d)
+    ld = torch.tensor([-0.3], device="cuda")
+    cu = torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32)
+    o, S = gdr.linear_forward(q, k, v, log_decay=ld, initial_state=S0, cu_seqlens=cu)
+    fine()
+    q, k, v, S0, o, S = (x.cpu() for x in (q, k, v, S0, o, S))
+    t = 0
+    for n, L in enumerate(lens):
+        s = slice(t, t + L)
+        ref.check_forward(q[0, s], k[0, s], v[0, s], ld, S0[n], 1.0, o[0, s], S[n], f"sequence {n}")
+        t += L
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_offsets_beyond_32_bits(dtype):
+    """Tokens 2^27 elements apart: the last ones start past element 2^32 of their buffer."""
+    T, d, far = 34, 64, 1 << 27
+    flat = torch.empty((T - 1) * far + d, device="cuda", dtype=dtype)
+    wide = flat.as_strided((1, T, 1, d), (d, far, d, 1))
+    q, k, v, _ = tensors(41, 1, T, 1, 1, d, d, dtype)
+    ld = torch.tensor([-0.1], device="cuda")
+    want = gdr.linear_forward(q, k, v, log_decay=ld)
+    grads = gdr.linear_backward(q, k, v, v, log_decay=ld)
+    wide.copy_(v)
+    got = gdr.linear_forward(q, k, wide, log_decay=ld)
+    back = gdr.linear_backward(q, k, wide, wide, log_decay=ld)
+    fine()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(torch.equal(back[n], grads[n]) for n in grads)
+
+
+def test_pool_beyond_32_bits():
+    """A pool of more than 2^31 elements: the pages behind that."""
+    H, d, pages = 2, 128, 66000
+    pool = torch.empty(pages, H, d, d, device="cuda")
+    last = [pages - 1, pages - 2, 65536, 0]
+    start = randn(gen(42), 4, H, d, d)
+    gdr.copy_states(pool, [-1] * 4, last)
+    for p, s in zip(last, start):
+        pool[p] = s
+    small = start.clone()
+    g = gen(43)
+    slots = torch.tensor(last, device="cuda", dtype=torch.int32)
+    ld = torch.tensor([-0.1, -0.01], device="cuda")
+    q, k, v = (randn(g, 4, H, d, dtype=BF16) for _ in range(3))
+    a = gdr.linear_decode_step(q, k, v, pool, log_decay=ld, state_slots=slots)
+    b = gdr.linear_decode_step(q, k, v, small, log_decay=ld)
+    assert torch.equal(a, b)
+    q, k, v = (randn(g, 1, 100, H, d, dtype=BF16) for _ in range(3))
+    cu = torch.tensor([0, 10, 40, 90, 100], device="cuda", dtype=torch.int32)
+    a = gdr.linear_forward(q, k, v, log_decay=ld, initial_state=pool, final_state=pool, cu_seqlens=cu, state_slots=slots)
+    b = gdr.linear_forward(q, k, v, log_decay=ld, initial_state=small, final_state=small, cu_seqlens=cu)
+    assert torch.equal(a[0], b[0]) and all(torch.equal(pool[p], s) for p, s in zip(last, small))
+    gdr.copy_states(pool, last[:2], [7, pages - 3])
+    fine()
+    assert torch.equal(pool[7], small[0]) and torch.equal(pool[pages - 3], small[1])
+
+
+def test_padding_rows_with_any_contents():
+    """A decode row without a page may hold anything, and equal padding slots are fine."""
+    q, k, v = (torch.full((3, 2, 64), float("nan"), device="cuda", dtype=BF16) for _ in range(3))
+    g = gen(44)
+    for x in (q, k, v):
+        x[1] = randn(g, 2, 64, dtype=BF16)
+    pool = randn(g, 2, 2, 64, 64)
+    before, one = pool.clone(), pool[1:].clone()
+    ld = torch.tensor([-0.1, 0.0], device="cuda")
+    o = gdr.linear_decode_step(q, k, v, pool, log_decay=ld,
+                               state_slots=torch.tensor([-1, 1, -1], device="cuda", dtype=torch.int32))
+    o1 = gdr.linear_decode_step(q[1:2].contiguous(), k[1:2].contiguous(), v[1:2].contiguous(), one, log_decay=ld)
+    fine()
+    assert (o[0] == 0).all() and (o[2] == 0).all() and torch.equal(o[1:2], o1)
+    assert torch.equal(pool[0], before[0]) and torch.equal(pool[1:], one)
