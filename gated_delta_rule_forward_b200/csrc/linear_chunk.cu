@@ -376,7 +376,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<uint32_t *>(sm + M::SLOT);   // 0: the CTA holds all of tensor memory (the MMA warp writes it so)
-  griddep_launch_dependents();
 
   const int page = lin_page(p, it.n);
   // (the end state of a sequence with several segments is made from phase 1's)
@@ -389,7 +388,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   // The grid before: phase 1's states, or the chain kernel's.  (A sequence that runs whole
   // needs nothing of it, and may run beside it.)
   const float *start = r.X + static_cast<size_t>(it.slot) * DA * DC;
-  if (PHASE1 || it.nseg > 1) griddep_wait();
+  if (!sel.beside && (PHASE1 || it.nseg > 1)) griddep_wait();
+  griddep_launch_dependents();
   if (!PHASE1 && it.nseg > 1 && !p.chained) {
     float *mine = r.XS + static_cast<size_t>(it.slot) * DA * DC;
     lin_self_chain(p, r, it, page, last, DA, DC, mine, tid, NTHREADS);
@@ -411,6 +411,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int j = i > NST ? i - NST : 0; j < i; ++j)
         mbar_wait(reinterpret_cast<uint64_t *>(sm + M::LOAD) + j % NST, (j / NST) & 1);
     }
+    if (sel.beside) griddep_wait();   // what follows this grid follows the one beside it
   } else if (warp > W_COPY) {
     // ---------------------------------------------------------------- MMAs
     // A warp for each kind, so that none waits behind another's operands; a product's
@@ -906,8 +907,10 @@ cudaError_t gdr_launch_linear_chunk(const gdr::LinProblem &p, const gdr::LinChun
       sel.run[sel.n++] = j;
       done[j] = true;
     }
-    // a programmatic dependent waits for the one launch before it, so only the phase's first one may be it
-    const bool dep = pdl && i == 0;
+    // the phase's first launch waits for the phase before; the others start once all of its CTAs are past that
+    // wait, run beside it and end after it
+    sel.beside = i > 0;
+    const bool dep = pdl || sel.beside;
     const cudaError_t e = phase1    ? gdr::tc::launch_shape<true, false>(a.da, a.dc, p, maps, sel, dep, s)
                           : a.y_f32 ? gdr::tc::launch_shape<false, true>(a.da, a.dc, p, maps, sel, dep, s)
                                     : gdr::tc::launch_shape<false, false>(a.da, a.dc, p, maps, sel, dep, s);

@@ -14,6 +14,7 @@ struct LinChunkMaps {
 struct LinRunSel {
   int n;
   int run[kLinMaxRuns];
+  bool beside;   // a programmatic dependent of another launch of its phase, with which it shares only inputs
 };
 
 }  // namespace gdr

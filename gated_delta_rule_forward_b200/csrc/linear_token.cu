@@ -27,18 +27,24 @@ __device__ __forceinline__ void copy16(uint32_t dst, const float *src) {
 }
 
 template <int DA, int DC, bool PHASE1>
-__global__ void __launch_bounds__(DC * 4) linear_token_kernel(const __grid_constant__ LinProblem p, int ir) {
+__global__ void __launch_bounds__(DC * 4) linear_token_kernel(const __grid_constant__ LinProblem p, int ir,
+                                                              bool beside) {
   constexpr int R = DA / 32, NT = DC * 4;
   __shared__ __align__(16) float ta[2][PHASE1 ? 1 : TT][DA], tb[2][TT][DA], tcol[2][TT][DC];
+  // In every thread, at the start or (a run beside the phase's first) at the end: a grid may not
+  // end before the one it depends on.
+  if (!beside) tc::griddep_wait();
   tc::griddep_launch_dependents();
-  tc::griddep_wait();   // in every thread: this grid may not end before the one it depends on
   const LinRun &r = p.run[ir];
   const int tid = threadIdx.x, lane = tid & 31, c0 = 8 * (tid >> 5);
   const LinItem it = lin_item(p, blockIdx.x);
   const int h = it.h;
   const bool rev = r.reverse != 0;
   const bool last = rev ? it.g == 0 : it.g == it.nseg - 1;    // in the run's order
-  if (!it.ok || (PHASE1 && last && (it.nseg == 1 || !r.s_final))) return;
+  if (!it.ok || (PHASE1 && last && (it.nseg == 1 || !r.s_final))) {
+    if (beside) tc::griddep_wait();
+    return;
+  }
   const float ld = __ldg(p.log_decay + h);
   const int page = lin_page(p, it.n);
 
@@ -166,6 +172,7 @@ __global__ void __launch_bounds__(DC * 4) linear_token_kernel(const __grid_const
 #pragma unroll
       for (int c = 0; c < 4; ++c) *reinterpret_cast<uint64_t *>(dst + (lane + 32 * i) * DC + c0 + 2 * c) = S[i][c];
   }
+  if (beside) tc::griddep_wait();
 }
 
 template <int DA, int DC, bool PHASE1>
@@ -179,7 +186,7 @@ cudaError_t launch_run(const LinProblem &p, int ir, bool pdl, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, linear_token_kernel<DA, DC, PHASE1>, p, ir);
+  return cudaLaunchKernelEx(&cfg, linear_token_kernel<DA, DC, PHASE1>, p, ir, ir > 0);
 }
 
 template <bool PHASE1>
@@ -196,8 +203,9 @@ cudaError_t launch_shape(const LinProblem &p, int ir, bool pdl, cudaStream_t s) 
 
 cudaError_t gdr_launch_linear_token(const gdr::LinProblem &p, bool phase1, bool pdl, cudaStream_t s) {
   for (int i = 0; i < p.nrun; ++i) {
-    // a programmatic dependent waits for the one launch before it, so only the phase's first one may be it
-    const bool dep = pdl && i == 0;
+    // the first run waits for the phase before; the others start once all of its CTAs are past that wait, run
+    // beside it and end after it
+    const bool dep = pdl || i > 0;
     const cudaError_t e = phase1 ? gdr::launch_shape<true>(p, i, dep, s) : gdr::launch_shape<false>(p, i, dep, s);
     if (e != cudaSuccess) return e;
   }
