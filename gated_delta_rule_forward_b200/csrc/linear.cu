@@ -130,25 +130,31 @@ cudaError_t gdr_launch_linear_group_sum(const float *x, void *y, bool bf16, int 
   return cudaGetLastError();
 }
 
-// bf16, a dense batch: one CTA per SM and (run, segment, head).  Times in us on a B200 with
-// its clock under load: a round of CTAs costs kStart, and a chunk of 64 tokens kChunk2 with
-// outputs, kChunk1 in phase 1; less where half of the SMs stay idle, whose power the others get.
-// (64 sequences of 32 chunks: whole 66 us, in two segments each 58, in four 74; 192 runs of 32
-// chunks whole 110, in two 139; 16 of 1024 in nine segments 345, in eight 348, in 18 349, in four 491.)
+// A dense batch: CTAs of one (run, segment, head), each with an SM of its own (or, fp32 at value
+// widths of 64, half of one).  Times in us on a B200: a round of CTAs costs `start`, a
+// step of 64 (bf16) or 16 (fp32) tokens `step2` with outputs and `step1` in phase 1.
+// bf16 has the clock it has under load, and less of a cost where half of the SMs stay idle, whose
+// power the others get.
+// (bf16: 64 sequences of 32 chunks: whole 66 us, in two segments each 58, in four 74; 192 runs of
+// 32 chunks whole 110, in two 139; 16 of 1024 in nine segments 345, in eight 348, in 18 349, in
+// four 491.)
 namespace {
-constexpr float kStart = 5.f, kChunk1 = 1.15f, kChunk2 = 2.1f, kChunk2Half = 1.9f, kSelfChain = 1.5f, kChainKernel = 8.f;
+struct PlanCost {
+  float start, step1, step2, step2_half;
+};
+constexpr PlanCost kChunkCost = {5.f, 1.15f, 2.1f, 1.9f}, kTokenCost = {4.f, 4.3f, 6.1f, 6.1f};
+// a phase 2 that chains its states, for each segment before the last, and the kernel
+constexpr float kSelfChain = 1.4f, kChainKernel = 3.5f;
 
-int plan_dense(const gdr::LinProblem &p, int sms) {   // segments per sequence
+int plan_dense(const gdr::LinProblem &p, const PlanCost &cost, int steps, int slots) {   // segments per sequence
   const long units = static_cast<long>(p.N) * p.H * p.nrun;
-  const int nc = (p.T + 63) / 64;
   float best = 0.f;
   int G = 1;
-  for (int g = 1; g <= 64 && (g == 1 || 2 * g <= nc); ++g) {
-    const int len = (nc + g - 1) / g;
-    const long rounds = (units * g + sms - 1) / sms;
-    const float chunk2 = 2 * units * g <= sms ? kChunk2Half : kChunk2;
-    float t = rounds * (kStart + len * chunk2);
-    if (g > 1) t += rounds * (kStart + len * kChunk1) + (g <= gdr::kLinSelfChain ? kSelfChain * (g - 1) : kChainKernel);
+  for (int g = 1; g == 1 || (g <= steps && units * g <= 2l * slots); ++g) {
+    const int len = (steps + g - 1) / g;
+    const long rounds = (units * g + slots - 1) / slots;
+    float t = rounds * (cost.start + len * (2 * units * g <= slots ? cost.step2_half : cost.step2));
+    if (g > 1) t += rounds * (cost.start + len * cost.step1) + (g <= gdr::kLinSelfChain ? kSelfChain * (g - 1) : kChainKernel);
     if (g == 1 || t < best) {
       best = t;
       G = g;
@@ -159,25 +165,20 @@ int plan_dense(const gdr::LinProblem &p, int sms) {   // segments per sequence
 }  // namespace
 
 void gdr_linear_plan(gdr::LinProblem *p, int sms) {
-  const long total = static_cast<long>(p->B) * p->T, units = static_cast<long>(p->N) * p->H * p->nrun;
+  const long total = static_cast<long>(p->B) * p->T;
+  const int step = p->bf16_io ? 64 : 16;
   long seg;
-  if (p->bf16_io) {
-    if (!p->cu) {
-      const int nc = (p->T + 63) / 64, g = plan_dense(*p, sms);
-      seg = 64l * ((nc + g - 1) / g);
-    } else {
-      // lengths unknown here: segments that give every SM one (a packed batch of 9200 tokens, 16 heads:
-      // 1024 tokens 83 us, 512: 95, 2048: 111)
-      seg = total * p->H * p->nrun / sms;
-      if (seg < 256) seg = 256;
-    }
-    seg = (seg + 63) / 64 * 64;
+  if (!p->cu) {
+    const int steps = (p->T + step - 1) / step;
+    bool narrow = true;
+    for (int i = 0; i < p->nrun; ++i) narrow = narrow && p->run[i].dc == 64;
+    const int g = plan_dense(*p, p->bf16_io ? kChunkCost : kTokenCost, steps, !p->bf16_io && narrow ? 2 * sms : sms);
+    seg = static_cast<long>(step) * ((steps + g - 1) / g);
   } else {
-    // token kernel: three CTAs or so per SM
-    seg = total * p->H * p->nrun / (3L * sms);
-    seg = (seg + 15) / 16 * 16;
-    if (seg < 32) seg = 32;
-    if (!p->cu && units >= 2L * sms) seg = p->T;
+    // lengths unknown here: segments that give every SM one (a packed bf16 batch of 9200 tokens, 16 heads:
+    // 1024 tokens 83 us, 512: 95, 2048: 111)
+    seg = (total * p->H * p->nrun / sms + step - 1) / step * step;
+    if (seg < 4 * step) seg = 4 * step;
   }
   if (seg > p->T) seg = p->T;
   if (seg < 1) seg = 1;

@@ -161,10 +161,12 @@ __device__ __forceinline__ void lin_self_chain(const LinProblem &p, const LinRun
   const bool fin = last && r.s_final && page >= 0;
   const size_t at_page = (static_cast<size_t>(page < 0 ? 0 : page) * p.H + it.h) * elems;
   float f[kLinSelfChain];
+  {   // the decay over the run's k-th segment; a lane computes one of them
+    const int k = tid & 3, seg = r.reverse ? it.nseg - 1 - k : k;
+    static_assert(kLinSelfChain == 4, "lanes");
+    const float x = k < before + fin ? lin_pow64(ld, min(it.len, (seg + 1) * p.seg) - seg * p.seg) : 0.f;
 #pragma unroll
-  for (int k = 0; k < kLinSelfChain; ++k) {   // the run's k-th segment
-    const int seg = r.reverse ? it.nseg - 1 - k : k;
-    f[k] = k < before + fin ? lin_pow64(ld, min(it.len, (seg + 1) * p.seg) - seg * p.seg) : 0.f;
+    for (int i = 0; i < kLinSelfChain; ++i) f[i] = __shfl_sync(0xffffffffu, x, i);
   }
   for (int e = 4 * tid; e < static_cast<int>(elems); e += 4 * threads) {
     float4 d[kLinSelfChain];

@@ -3,12 +3,17 @@
 // tokens).
 //
 // One CTA owns one (run, segment, head), one warp of it eight columns of the
-// state; the da x 8 fp32 slice lives in registers (lane l holds rows l, l + 32,
-// ...; columns in pairs).  Tokens come through shared memory eight at a time,
-// the next eight on their way while these are computed.  Per token
-// S <- lambda S + b c^T and y = S^T a, the eight column sums reduced over the lanes
-// by halving exchanges (9 shuffles instead of 40).  Bound by issue: about 80
-// instructions a token and warp.
+// state; the da x 8 fp32 slice lives in registers (eight lanes share the rows of two
+// columns; rows in pairs).  Tokens come through shared memory sixteen at a time, the
+// next sixteen on their way while these are computed.  Per token S <- lambda S + b c^T
+// and y = S^T a; the sums of four tokens' columns go over the lanes together, seven
+// exchanges for eight of them.  (A reverse run is the same recurrence with the first
+// token's decay moved to the end.)
+//
+// Bound by the FMA pipe: 3 d^2 multiplications and additions a token are 200 ns of an
+// SM at d = 128; it takes 380 (the pipe 57% active).  Two sequences of 500 tokens, 4
+// heads: 33 us in a graph; 74 of 300, 8 heads: 460 us.  With a column's rows over all 32
+// lanes (nine exchanges a token) these were 43 and 636.
 #include "linear.cuh"
 #include "tc_util.cuh"
 
@@ -20,23 +25,24 @@ using tc::mul_f32x2;
 using tc::pair_f32;
 using tc::unpair_f32;
 
-constexpr int TT = 8;   // tokens a tile
+constexpr int TT = 16;   // tokens a tile
+constexpr int NC = 2;    // columns a lane
 
 __device__ __forceinline__ void copy16(uint32_t dst, const float *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 template <int DA, int DC, bool PHASE1>
-__global__ void __launch_bounds__(DC * 4) linear_token_kernel(const __grid_constant__ LinProblem p, int ir,
+__global__ void __launch_bounds__(DC * 8 / NC) linear_token_kernel(const __grid_constant__ LinProblem p, int ir,
                                                               bool beside) {
-  constexpr int R = DA / 32, NT = DC * 4;
+  constexpr int R = DA / 32, NT = DC * 8 / NC, HC = NC / 2;
   __shared__ __align__(16) float ta[2][PHASE1 ? 1 : TT][DA], tb[2][TT][DA], tcol[2][TT][DC];
   // In every thread, at the start or (a run beside the phase's first) at the end: a grid may not
   // end before the one it depends on.
   if (!beside) tc::griddep_wait();
   tc::griddep_launch_dependents();
   const LinRun &r = p.run[ir];
-  const int tid = threadIdx.x, lane = tid & 31, c0 = 8 * (tid >> 5);
+  const int tid = threadIdx.x, lane = tid & 31;
   const LinItem it = lin_item(p, blockIdx.x);
   const int h = it.h;
   const bool rev = r.reverse != 0;
@@ -48,11 +54,13 @@ __global__ void __launch_bounds__(DC * 4) linear_token_kernel(const __grid_const
   const float ld = __ldg(p.log_decay + h);
   const int page = lin_page(p, it.n);
 
-  uint64_t S[R][4];
+  // S[j][k][c]: rows row0 + 32 j + 2 k (+ 1), column col0 + c
+  const int row0 = 4 * (lane & 7), col0 = 4 * NC * (tid >> 5) + NC * (lane >> 3);
+  uint64_t S[R][2][NC];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+  for (int j = 0; j < R; ++j)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) S[i][c] = 0;
+    for (int k = 0; k < 2 * NC; ++k) S[j][k / NC][k % NC] = 0;
   if (!PHASE1) {
     const float *start = r.X + static_cast<size_t>(it.slot) * DA * DC;
     if (it.nseg > 1 && !p.chained) {
@@ -65,12 +73,22 @@ __global__ void __launch_bounds__(DC * 4) linear_token_kernel(const __grid_const
     if (whole) start = r.s0 && page >= 0 ? r.s0 + (static_cast<size_t>(page) * p.H + h) * DA * DC : nullptr;
     if (start)
 #pragma unroll
-      for (int i = 0; i < R; ++i)
+      for (int j = 0; j < R; ++j)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int row = lane + 32 * i, col = c0 + 2 * c;
-          S[i][c] = t ? pair_f32(start[col * DA + row], start[(col + 1) * DA + row])
-                      : *reinterpret_cast<const uint64_t *>(start + row * DC + col);
+        for (int k = 0; k < 2; ++k) {
+          const int row = row0 + 32 * j + 2 * k;
+          if (t) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) S[j][k][c] = *reinterpret_cast<const uint64_t *>(start + (col0 + c) * DA + row);
+          } else {
+#pragma unroll
+            for (int c = 0; c < NC; c += 2) {
+              const float2 x = *reinterpret_cast<const float2 *>(start + row * DC + col0 + c);
+              const float2 y = *reinterpret_cast<const float2 *>(start + (row + 1) * DC + col0 + c);
+              S[j][k][c] = pair_f32(x.x, y.x);
+              S[j][k][c + 1] = pair_f32(x.y, y.y);
+            }
+          }
         }
   }
 
@@ -102,10 +120,15 @@ __global__ void __launch_bounds__(DC * 4) linear_token_kernel(const __grid_const
   const float lam1 = off == 0. || lam0 == 0.f ? lam0 : __int_as_float(__float_as_int(lam0) + (off < 0. ? -1 : 1));
   const float share = lam1 == lam0 ? 0.f : static_cast<float>(off / (static_cast<double>(lam1) - lam0));
   float owed = 0.f;
-
-  // lanes with bit 4, 3, 2 clear keep the lower half of the columns each time
-  const int ycol = c0 + ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
-  float *y = static_cast<float *>(r.y) + ((static_cast<size_t>(it.b) * p.T + it.t0) * p.H + h) * DC + ycol;
+  auto decay = [&]() {
+    owed += share;
+    const bool up = owed > 0.5f;
+    owed -= up ? 1.f : 0.f;
+    return up ? lam1 : lam0;
+  };
+  // of four tokens' columns each lane of a row group sums up HC: token yt, columns col0 + HC yc ..
+  const int yc = (lane >> 2) & 1, yt = lane & 3;
+  float *y = static_cast<float *>(r.y) + ((static_cast<size_t>(it.b) * p.T + it.t0) * p.H + h) * DC + col0 + HC * yc;
   const size_t ystep = static_cast<size_t>(p.H) * DC;
   const float bscale = r.bscale, yscale = r.yscale;
   if (count > 0) fetch(0, 0);
@@ -118,59 +141,87 @@ __global__ void __launch_bounds__(DC * 4) linear_token_kernel(const __grid_const
     }
     __syncthreads();
     const int n = min(TT, count - i0);
-#pragma unroll 2
-    for (int t = 0; t < n; ++t) {
-      owed += share;
-      const bool up = owed > 0.5f;
-      owed -= up ? 1.f : 0.f;
-      const float lam = up ? lam1 : lam0;
-      const uint64_t l2 = pair_f32(lam, lam);
-      uint64_t c[4], y2[4] = {0, 0, 0, 0};
+#pragma unroll 1
+    for (int t0 = 0; t0 < n; t0 += 4) {
+      float v[4][NC] = {};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) c[k] = *reinterpret_cast<const uint64_t *>(&tcol[buf][t][c0 + 2 * k]);
+      for (int u = 0; u < 4; ++u) {
+        const int t = t0 + u;
+        if (t >= n) break;
+        const float lam = rev && i0 + t == 0 ? 1.f : decay();
+        const uint64_t l2 = pair_f32(lam, lam);
+        uint64_t c[NC], y2[NC] = {};
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const float b = bscale * tb[buf][t][lane + 32 * i];
-        const uint64_t b2 = pair_f32(b, b);
-        uint64_t a2 = 0;
-        if (!PHASE1) {
-          const float a = ta[buf][t][lane + 32 * i];
-          a2 = pair_f32(a, a);
+        for (int e = 0; e < NC; ++e) {
+          const float x = bscale * tcol[buf][t][col0 + e];
+          c[e] = pair_f32(x, x);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          S[i][k] = rev ? fma_f32x2(b2, c[k], S[i][k]) : fma_f32x2(l2, S[i][k], mul_f32x2(b2, c[k]));
-          if (!PHASE1) y2[k] = fma_f32x2(a2, S[i][k], y2[k]);
-          if (rev) S[i][k] = mul_f32x2(l2, S[i][k]);
+        for (int j = 0; j < R; ++j) {
+          const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(&tb[buf][t][row0 + 32 * j]);
+          ulonglong2 a = {0, 0};
+          if (!PHASE1) a = *reinterpret_cast<const ulonglong2 *>(&ta[buf][t][row0 + 32 * j]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < NC; ++e) {
+              const uint64_t b2 = k ? b.y : b.x;
+              uint64_t &s = S[j][k][e];
+              s = fma_f32x2(l2, s, mul_f32x2(b2, c[e]));
+              if (!PHASE1) y2[e] = fma_f32x2(k ? a.y : a.x, s, y2[e]);
+            }
         }
+        if (!PHASE1)
+#pragma unroll
+          for (int e = 0; e < NC; ++e) {
+            float lo, hi;
+            unpair_f32(y2[e], lo, hi);
+            v[u][e] = lo + hi;
+          }
       }
       if (!PHASE1) {
-        float v[8], z4[4], z2[2], z;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) unpair_f32(y2[k], v[2 * k], v[2 * k + 1]);
+        for (int c = 0; c < HC; ++c) {
+          float z4[4], z2[2], z;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          z4[k] = (lane & 16 ? v[k + 4] : v[k]) + __shfl_xor_sync(0xffffffffu, lane & 16 ? v[k] : v[k + 4], 16);
+          for (int u = 0; u < 4; ++u)
+            z4[u] = (yc ? v[u][HC + c] : v[u][c]) + __shfl_xor_sync(0xffffffffu, yc ? v[u][c] : v[u][HC + c], 4);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          z2[k] = (lane & 8 ? z4[k + 2] : z4[k]) + __shfl_xor_sync(0xffffffffu, lane & 8 ? z4[k] : z4[k + 2], 8);
-        z = (lane & 4 ? z2[1] : z2[0]) + __shfl_xor_sync(0xffffffffu, lane & 4 ? z2[0] : z2[1], 4);
-        z += __shfl_xor_sync(0xffffffffu, z, 2);
-        z += __shfl_xor_sync(0xffffffffu, z, 1);
-        if ((lane & 3) == 0) y[token(i0 + t) * ystep] = yscale * z;
+          for (int u = 0; u < 2; ++u)
+            z2[u] = (lane & 2 ? z4[u + 2] : z4[u]) + __shfl_xor_sync(0xffffffffu, lane & 2 ? z4[u] : z4[u + 2], 2);
+          z = (lane & 1 ? z2[1] : z2[0]) + __shfl_xor_sync(0xffffffffu, lane & 1 ? z2[0] : z2[1], 1);
+          if (t0 + yt < n) y[token(i0 + t0 + yt) * ystep + c] = yscale * z;
+        }
       }
     }
     __syncthreads();   // this tile is read before the one after the next replaces it
   }
 
+  if (rev && count > 0) {   // a reverse state is left with the decay to the next token applied
+    const float lam = decay();
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+      for (int k = 0; k < 2 * NC; ++k) S[j][k / NC][k % NC] = mul_f32x2(pair_f32(lam, lam), S[j][k / NC][k % NC]);
+  }
   float *dst = nullptr;
   if (PHASE1) dst = r.X + static_cast<size_t>(it.slot) * DA * DC;
   else if (it.nseg == 1 && r.s_final && page >= 0) dst = r.s_final + (static_cast<size_t>(page) * p.H + h) * DA * DC;
   if (dst) {
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int j = 0; j < R; ++j)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) *reinterpret_cast<uint64_t *>(dst + (lane + 32 * i) * DC + c0 + 2 * c) = S[i][c];
+      for (int k = 0; k < 2; ++k) {
+        float *to = dst + (row0 + 32 * j + 2 * k) * DC + col0;
+#pragma unroll
+        for (int c = 0; c < NC; c += 2) {
+          float2 x, y;
+          unpair_f32(S[j][k][c], x.x, y.x);
+          unpair_f32(S[j][k][c + 1], x.y, y.y);
+          *reinterpret_cast<float2 *>(to + c) = x;
+          *reinterpret_cast<float2 *>(to + DC + c) = y;
+        }
+      }
   }
   if (beside) tc::griddep_wait();
 }
@@ -179,7 +230,7 @@ template <int DA, int DC, bool PHASE1>
 cudaError_t launch_run(const LinProblem &p, int ir, bool pdl, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(lin_blocks(p)));
-  cfg.blockDim = dim3(DC * 4);
+  cfg.blockDim = dim3(DC * 8 / NC);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

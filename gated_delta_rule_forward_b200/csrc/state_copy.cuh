@@ -12,7 +12,7 @@ struct CopyPairs {
   int src[kMaxCopyPairs];   // -1: zeros
   int dst[kMaxCopyPairs];
 };
-// Up to these go as 256 bytes (a launch with 4 KB of arguments takes the host longer).
+// Up to these go as 256 bytes (8 pages forked: 10.5 us a call, with 4 KB of arguments 11.7).
 constexpr int kFewCopyPairs = 31;
 
 }  // namespace gdr

@@ -417,8 +417,9 @@ def test_empty_calls():
     fine()
 
 
-# (the number of segments that the plan takes on 148 SMs: 2, 3, 4, 4, more than 4)
-@pytest.mark.parametrize("dtype,T,Hk,H,dk,dv", [(BF16, 2048, 25, 50, 64, 64), (BF16, 1400, 18, 36, 64, 64),
+# (the plan takes 2, 3, 4 and, from the fourth on, many segments on 148 SMs)
+@pytest.mark.parametrize("dtype,T,Hk,H,dk,dv", [(BF16, 2048, 25, 50, 64, 64), (BF16, 1150, 24, 48, 64, 64),
+                                               (BF16, 1400, 18, 36, 64, 64),
                                                (BF16, 901, 1, 2, 128, 128), (BF16, 705, 2, 4, 64, 128),
                                                (BF16, 1700, 1, 3, 128, 64), (F32, 901, 1, 2, 128, 128)])
 def test_segments(dtype, T, Hk, H, dk, dv):
@@ -437,7 +438,9 @@ def test_segments(dtype, T, Hk, H, dk, dv):
     ref.check_forward(q[0], k[0], v[0], ld, S0[0], 0.1, o2[0], S2[0], "in place")
 
 
-@pytest.mark.parametrize("dtype,T,Hk,H,dk,dv,state", [(BF16, 2048, 6, 18, 64, 64, True), (BF16, 901, 1, 2, 128, 64, True),
+@pytest.mark.parametrize("dtype,T,Hk,H,dk,dv,state", [(BF16, 2048, 6, 18, 64, 64, True), (BF16, 1150, 16, 16, 64, 64, True),
+                                                     (BF16, 1400, 6, 12, 64, 64, True), (BF16, 901, 1, 2, 128, 64, True),
+                                                     (F32, 1500, 2, 16, 64, 64, True),
                                                      (BF16, 1100, 3, 3, 64, 128, False), (F32, 500, 1, 2, 64, 128, True)])
 def test_backward_segments(dtype, T, Hk, H, dk, dv, state):
     q, k, v, g = tensors(T + 4, 1, T, Hk, H, dk, dv, dtype)
@@ -530,3 +533,36 @@ def test_padding_rows_with_any_contents():
     fine()
     assert (o[0] == 0).all() and (o[2] == 0).all() and torch.equal(o[1:2], o1)
     assert torch.equal(pool[0], before[0]) and torch.equal(pool[1:], one)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_changing_decays_and_offsets(dtype):
+    """Decays, offsets and slots overwritten on the stream between two calls are the second call's."""
+    lens = [[300, 1, 600], [2, 800, 99]]
+    H, d = 2, 128
+    g = gen(51)
+    q, k, v, do = (randn(g, 1, 901, H, d, dtype=dtype) for _ in range(4))
+    lds = [torch.tensor([-0.1, -1.0], device="cuda"), torch.tensor([-2.0, -0.01], device="cuda")]
+    cus = [torch.tensor([0] + x, device="cuda").cumsum(0).to(torch.int32) for x in lens]
+    slots = [torch.tensor(x, device="cuda", dtype=torch.int32) for x in ([2, 0, 1], [0, 1, 2])]
+    start = randn(g, 3, H, d, d)
+
+    def call(ld, cu, slot):
+        pool = start.clone()
+        o, _ = gdr.linear_forward(q, k, v, log_decay=ld, initial_state=pool, final_state=pool, cu_seqlens=cu,
+                                  state_slots=slot)
+        x = gdr.linear_backward(q, k, v, do, log_decay=ld, initial_state=start, cu_seqlens=cu)
+        dense = gdr.linear_forward(q, k, v, log_decay=ld)
+        return [o, pool, *dense, *x.values()]
+
+    want = [call(lds[i], cus[i], slots[i]) for i in range(2)]
+    torch.cuda.synchronize()
+    args = [lds[0].clone(), cus[0].clone(), slots[0].clone()]
+    got = []
+    for i in (0, 1, 0):
+        for a, b in zip(args, (lds[i], cus[i], slots[i])):
+            a.copy_(b)
+        got.append((i, call(*args)))
+    fine()
+    for i, x in got:
+        assert all(torch.equal(a, b) for a, b in zip(x, want[i]))
