@@ -545,6 +545,9 @@ gdr_status_t gdr_linear_backward(int dtype, int B, int T, int Hk, int H, int dk,
   if ((st = linear_states(a)) != GDR_OK) return st;
   if ((g->d_final_state && !aligned16(g->d_final_state)) || (g->d_initial_state && !aligned16(g->d_initial_state)))
     return fail(GDR_ERR_ALIGNMENT, "state pointers must be 16-byte aligned");
+  // the runs read both states side by side with the one that writes this
+  if (g->d_initial_state && (g->d_initial_state == g->d_final_state || g->d_initial_state == a->initial_state))
+    return fail(GDR_ERR_INVALID_ARG, "d_initial_state must not be d_final_state or initial_state");
   if (!a->log_decay) return fail(GDR_ERR_INVALID_ARG, "log_decay is required");
   gdr::LinProblem p;
   linear_shape(&p, dtype, B, T, H, dk, dv, N, a->cu_seqlens != nullptr, true);

@@ -90,6 +90,13 @@ def test_backward_missing(L, field):
     assert bwd(L, g=grads(**{field: None})) == 1
 
 
+def test_backward_state_written_over_one_it_reads(L):
+    other = FAKE + 0x10000
+    assert bwd(L, g=grads(d_final_state=FAKE)) == 1                    # d_initial_state itself
+    assert bwd(L, a=args(initial_state=FAKE), g=grads(d_final_state=other)) == 1
+    assert bwd(L, a=args(initial_state=other), g=grads(d_final_state=other)) == 4
+
+
 def test_null_structs_and_slots(L):
     assert L.gdr_linear_forward(*dims(), None, 1.0, None, 0, None) == 1
     assert L.gdr_linear_backward(*dims(), ctypes.byref(args()), None, 1.0, None, 0, None) == 1
