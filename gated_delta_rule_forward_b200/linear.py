@@ -120,7 +120,8 @@ def linear_forward(q, k, v, *, log_decay, initial_state=None, output_final_state
     initial_state and final_state are pools [pages,H,dk,dv] and sequence n's
     states lie in page state_slots[n], which must differ from one another; a slot
     outside the pool reads zeros and writes nothing.  final_state may be
-    initial_state.  Returns (o [B,T,H,dv], final_state or None).
+    initial_state; otherwise ``out`` and final_state overlap no input.  Returns
+    (o [B,T,H,dv], final_state or None).
     """
     a, dims = _shape(q, k, v, log_decay, cu_seqlens)
     dt, B, T, Hk, H, dk, dv, N = dims
@@ -181,7 +182,7 @@ def linear_backward(q, k, v, d_o, *, log_decay, initial_state=None, d_final_stat
         g.d_final_state = d_final_state.data_ptr()
     where, handle = _on(dev, stream)
     with where:
-        new = torch.empty if cu_seqlens is None else torch.zeros
+        new = torch.empty if cu_seqlens is None and v.shape[2] else torch.zeros   # no value heads: sums of nothing
         grads = {"q": new(B, T, Hk, dk, device=dev, dtype=q.dtype), "k": new(B, T, Hk, dk, device=dev, dtype=q.dtype),
                  "v": new(B, T, H, dv, device=dev, dtype=q.dtype),
                  "initial_state": torch.empty(N, H, dk, dv, device=dev, dtype=f32)}

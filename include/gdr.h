@@ -355,7 +355,8 @@ size_t gdr_linear_workspace_size(int dtype, int B, int T, int Hk, int H, int dk,
  * bf16 or fp32.  bf16 products run on the tensor cores with fp32 accumulation;
  * the state is carried in fp32 and its update keeps fp32 accuracy; fp32 inputs
  * are computed in fp32.  An empty sequence copies its initial state to its
- * final state.  The workspace (16-byte aligned, overwritten) may be NULL where
+ * final state.  The workspace (16-byte aligned, overwritten, not shared with a
+ * call or graph that may run at the same time) may be NULL where
  * gdr_linear_workspace_size() is 0.
  */
 gdr_status_t gdr_linear_forward(int dtype, int B, int T, int Hk, int H, int dk, int dv, int N,
@@ -370,7 +371,7 @@ gdr_status_t gdr_linear_forward(int dtype, int B, int T, int Hk, int H, int dk, 
  *     dq_t = scale S_t d_o_t,  dk_t = dS_t v_t,  dv_t = dS_t^T k_t,  dS_init = lambda dS_0
  * dq and dk are summed over the value heads that share a key head, in fp32 and
  * in a fixed order.  The decays are constants of the layer and have no
- * gradient.
+ * gradient.  A call without value heads (H = 0) or sequences writes nothing.
  */
 gdr_status_t gdr_linear_backward(int dtype, int B, int T, int Hk, int H, int dk, int dv, int N,
                                  const gdr_linear_args_t *args, const gdr_linear_grads_t *grads, float scale,

@@ -400,6 +400,61 @@ def test_repeatable_captured_and_on_streams():
         assert all(torch.equal(a, b) for a, b in zip(r, want2))
 
 
+def test_decode_captured():
+    """A replayed decode step reads the slots and tokens of its buffers as they are at the replay."""
+    N, H, dk, dv = 5, 2, 128, 64
+    g, ld = gen(31), torch.tensor([-0.05, -1.0], device="cuda")
+    q, k, v = (randn(g, N, H, d, dtype=BF16) for d in (dk, dk, dv))
+    slots = torch.tensor([4, 0, -1, 6, 2], device="cuda", dtype=torch.int32)
+    start = randn(g, 7, H, dk, dv)
+    state, o = start.clone(), torch.empty(N, H, dv, device="cuda", dtype=BF16)
+    gdr.linear_decode_step(q, k, v, state, log_decay=ld, state_slots=slots, scale=0.1, out=o)    # before the capture
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdr.linear_decode_step(q, k, v, state, log_decay=ld, state_slots=slots, scale=0.1, out=o)
+    for turn, rows in enumerate(([4, 0, -1, 6, 2], [1, 9, 3, 0, -1])):
+        for x in (q, k, v):
+            x.copy_(randn(g, *x.shape, dtype=BF16))
+        slots.copy_(torch.tensor(rows, dtype=torch.int32))
+        state.copy_(start)
+        want_state = start.clone()
+        graph.replay()
+        want = gdr.linear_decode_step(q, k, v, want_state, log_decay=ld, state_slots=slots, scale=0.1)
+        fine()
+        assert torch.equal(o, want) and torch.equal(state, want_state), turn
+        assert (o[[i for i, r in enumerate(rows) if not 0 <= r < 7]] == 0).all()
+
+
+def test_two_graphs_at_once():
+    """Two captured calls in segments, replayed on two streams at the same time: each has its own workspace."""
+    ld = torch.tensor([-0.01, -0.2], device="cuda")
+    inputs, graphs, got, want = [], [], [], []
+    for seed in (41, 42):
+        q, k, v, g = tensors(seed, 1, 3000, 1, 2, 128, 64, BF16)
+        do = randn(g, 1, 3000, 2, 64, dtype=BF16)
+        inputs.append((q, k, v, do))      # they live as long as the graphs
+
+        def call():
+            o, S = gdr.linear_forward(q, k, v, log_decay=ld)
+            x = gdr.linear_backward(q, k, v, do, log_decay=ld, d_final_state=S)
+            return [o, S, x["q"], x["k"], x["v"], x["initial_state"]]
+
+        want.append(call())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got.append(call())
+        graphs.append(graph)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(4):
+        for stream, graph in zip(streams, graphs):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    fine()
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def test_empty_calls():
     ld = decays(2)
     e = lambda *s, dt=BF16: torch.zeros(*s, device="cuda", dtype=dt)
@@ -414,6 +469,17 @@ def test_empty_calls():
     assert (x["initial_state"] == 0).all()
     assert gdr.linear_decode_step(e(0, 2, 64), e(0, 2, 64), e(0, 2, 64), e(3, 2, 64, 64, dt=F32), log_decay=ld,
                                   state_slots=e(0, dt=torch.int32)).shape == (0, 2, 64)
+    fine()
+
+
+def test_backward_without_value_heads():
+    for shape, cu in (((2, 5), None), ((1, 5), torch.tensor([0, 4], dtype=torch.int32, device="cuda"))):
+        q = randn(gen(2), *shape, 2, 64, dtype=BF16)
+        v = torch.empty(*shape, 0, 64, dtype=BF16, device="cuda")
+        torch.full((64, 64), 7.0, device="cuda")                   # freed: what a fresh tensor may hold
+        x = gdr.linear_backward(q, q, v, v, log_decay=decays(0), cu_seqlens=cu)
+        assert (x["q"] == 0).all() and (x["k"] == 0).all() and x["v"].shape == v.shape
+        assert x["q"].shape == q.shape and x["initial_state"].numel() == 0
     fine()
 
 
