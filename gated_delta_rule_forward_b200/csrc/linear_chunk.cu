@@ -35,11 +35,12 @@
 //     output (8 warps)   P of chunk i + 1 to bf16, the rows of chunk i
 // Only S -> operand -> O1 is a chain from chunk to chunk.
 //
-// Measured on a B200 (bf16, d = 128): 65536 tokens of 16 heads 373 us, both phases, with the
-// clock at 1.33 GHz under the power limit, which is what bounds it (291 us at 1.64 GHz: 113
-// and 178, the second 6.2 TB/s); 8 sequences of 2048 tokens, 8 heads, 61 us forward and 115 us
-// backward.  At the full clock the tensor pipe is active 50% of the time and 61% of the issue
-// slots are taken; a chunk takes about 2500 cycles.  Products: 64 KB of P's operands and so on
+// Measured on a B200 (bf16, d = 128): 65536 tokens of 16 heads, both phases, 307 us in ten
+// calls after a rest and 364 us after seconds of them, when the power limit holds the clock at
+// 1.30 GHz; 8 sequences of 2048 tokens, 8 heads, 59 us forward (1.73 GHz) and 112 us backward.
+// With 192 runs of 32 chunks the tensor pipe is active 42% of the time and 53% of the issue
+// slots are taken (1.73 GHz); a chunk takes about 2500 cycles, and value widths of 64 hardly
+// less (144 runs of 32 chunks: 67 us for 72).  Products: 64 KB of P's operands and so on
 // would take 1300.  Dropped after measurement: O1 and O2 in one accumulator (64k 385 us, backward
 // 118), one issuing warp for all products (404), weighting with packed bf16 arithmetic (no change).
 #include <atomic>
