@@ -42,7 +42,7 @@ class LinearArgs(ctypes.Structure):
     _fields_ = ([(name, ctypes.c_void_p) for name in ("q", "k", "v")]
                 + [(name, ctypes.c_longlong * 3) for name in ("q_stride", "k_stride", "v_stride")]
                 + [(name, ctypes.c_void_p) for name in ("log_decay", "cu_seqlens", "state_slots")]
-                + [("pages", ctypes.c_int)]
+                + [(name, ctypes.c_int) for name in ("pages", "zero_rest")]
                 + [(name, ctypes.c_void_p) for name in ("initial_state", "final_state", "o")])
 
 

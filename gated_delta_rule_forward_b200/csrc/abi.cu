@@ -525,6 +525,7 @@ gdr_status_t gdr_linear_forward(int dtype, int B, int T, int Hk, int H, int dk, 
   if (T == 0 && !a->final_state) return GDR_OK;
   if (injected_launch_fault()) return fail(GDR_ERR_CUDA, "injected launch failure (GDR_FAULT=launch)");
   p.cu = a->cu_seqlens; p.slots = a->state_slots; p.pages = a->state_slots ? a->pages : N;
+  p.zero_rest = a->cu_seqlens && a->zero_rest;
   p.log_decay = a->log_decay;
   gdr::LinRun &r = p.run[0];
   r.yscale = scale; r.y = a->o; r.s0 = a->initial_state; r.s_final = a->final_state;
@@ -568,6 +569,7 @@ gdr_status_t gdr_linear_backward(int dtype, int B, int T, int Hk, int H, int dk,
   if (T == 0 && !g->d_initial_state) return GDR_OK;
   if (injected_launch_fault()) return fail(GDR_ERR_CUDA, "injected launch failure (GDR_FAULT=launch)");
   p.cu = a->cu_seqlens; p.pages = N;
+  p.zero_rest = a->cu_seqlens && a->zero_rest;
   p.log_decay = a->log_decay;
   float *dq32 = nullptr, *dk32 = nullptr;
   if (H != Hk && T > 0) {
@@ -586,9 +588,9 @@ gdr_status_t gdr_linear_backward(int dtype, int B, int T, int Hk, int H, int dk,
   cudaError_t e = gdr_launch_linear(p, workspace, s, &err);
   if (e == cudaSuccess && dq32) {
     err = "group sum: ";
-    e = gdr_launch_linear_group_sum(dq32, g->dq, dtype == GDR_BF16, B, T, Hk, H / Hk, dk, a->cu_seqlens, N, s);
+    e = gdr_launch_linear_group_sum(dq32, g->dq, p, Hk, dk, s);
     if (e == cudaSuccess)
-      e = gdr_launch_linear_group_sum(dk32, g->dk, dtype == GDR_BF16, B, T, Hk, H / Hk, dk, a->cu_seqlens, N, s);
+      e = gdr_launch_linear_group_sum(dk32, g->dk, p, Hk, dk, s);
   }
   if (e != cudaSuccess) return fail(GDR_ERR_CUDA, "linear backward: " + err + cudaGetErrorString(e));
   return GDR_OK;

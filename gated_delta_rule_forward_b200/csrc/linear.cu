@@ -80,18 +80,22 @@ __global__ void __launch_bounds__(kChainThreads) linear_chain_kernel(const LinPr
 // group's values read in head order (so the order of the sum is fixed).
 template <typename IO>
 __global__ void __launch_bounds__(256) group_sum_kernel(const float *__restrict__ x, IO *__restrict__ y, long rows,
-                                                        int Hk, int G, int d, const int *cu, int N) {
+                                                        int Hk, int G, int d, const int *cu, int N, int zero_rest) {
   const long i = static_cast<long>(blockIdx.x) * 256 + threadIdx.x;   // 4 elements of one (row, key head)
   const int d4 = d / 4;
   const long rh = i / d4;
   const long row = rh / Hk;
   if (row >= rows) return;
-  if (cu && (row < __ldg(cu) || row >= __ldg(cu + N))) return;   // a row of no sequence
-  const float4 *src = reinterpret_cast<const float4 *>(x) + rh * G * d4 + i % d4;
-  float4 s = src[0];
-  for (int g = 1; g < G; ++g) {
-    const float4 v = src[static_cast<size_t>(g) * d4];
-    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  const bool none = cu && (row < __ldg(cu) || row >= __ldg(cu + N));   // a row of no sequence
+  if (none && !zero_rest) return;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (!none) {
+    const float4 *src = reinterpret_cast<const float4 *>(x) + rh * G * d4 + i % d4;
+    s = src[0];
+    for (int g = 1; g < G; ++g) {
+      const float4 v = src[static_cast<size_t>(g) * d4];
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
   }
   IO *dst = y + i * 4;
   st_io<IO>(dst, s.x);
@@ -119,14 +123,16 @@ cudaError_t gdr_launch_linear_chain(const gdr::LinProblem &p, bool pdl, cudaStre
   return cudaLaunchKernelEx(&cfg, linear_chain_kernel, p);
 }
 
-cudaError_t gdr_launch_linear_group_sum(const float *x, void *y, bool bf16, int B, int T, int Hk, int G, int d,
-                                        const int *cu, int N, cudaStream_t s) {
+cudaError_t gdr_launch_linear_group_sum(const float *x, void *y, const gdr::LinProblem &p, int Hk, int d, cudaStream_t s) {
   using namespace gdr;
-  const long rows = static_cast<long>(B) * T;
+  const int G = p.H / Hk;
+  const long rows = static_cast<long>(p.B) * p.T;
   const long threads = rows * Hk * (d / 4);
   const unsigned grid = static_cast<unsigned>((threads + 255) / 256);
-  if (bf16) group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(x, static_cast<__nv_bfloat16 *>(y), rows, Hk, G, d, cu, N);
-  else group_sum_kernel<float><<<grid, 256, 0, s>>>(x, static_cast<float *>(y), rows, Hk, G, d, cu, N);
+  if (p.bf16_io)
+    group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(x, static_cast<__nv_bfloat16 *>(y), rows, Hk, G, d, p.cu, p.N, p.zero_rest);
+  else
+    group_sum_kernel<float><<<grid, 256, 0, s>>>(x, static_cast<float *>(y), rows, Hk, G, d, p.cu, p.N, p.zero_rest);
   return cudaGetLastError();
 }
 

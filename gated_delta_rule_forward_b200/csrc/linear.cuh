@@ -64,6 +64,7 @@ struct LinProblem {
   int G;                 // segments of a sequence (packed: at most)
   int items;             // (sequence, segment) pairs (packed: an upper bound)
   int chained;           // X holds start states already (the chain kernel ran)
+  int zero_rest;         // the outputs' rows of no packed sequence become zeros
 };
 
 // A run's blocks are its segments of every head; each has a state in X.
@@ -134,6 +135,17 @@ __device__ __forceinline__ LinItem lin_item(const LinProblem &p, int block) {
   it.beg = it.g * p.seg;
   it.end = min(it.len, it.beg + p.seg);
   return it;
+}
+
+// This block's share of the zeros in a run's output rows of no sequence: [0, first) and [end, T), the offsets
+// cu[0] and cu[N].
+__device__ __forceinline__ void lin_zero_rest(const LinProblem &p, void *y, size_t row_bytes, int first, int end,
+                                              unsigned block, unsigned blocks) {
+  uint4 *const v = static_cast<uint4 *>(y);
+  const size_t row = row_bytes / 16, step = static_cast<size_t>(blocks) * blockDim.x;
+  const size_t mine = static_cast<size_t>(block) * blockDim.x + threadIdx.x;
+  for (size_t i = mine; i < first * row; i += step) v[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (size_t i = end * row + mine; i < p.T * row; i += step) v[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // lambda^n by way of 64 bits.
@@ -221,10 +233,9 @@ void gdr_linear_plan(gdr::LinProblem *p, int sms);
 size_t gdr_linear_workspace_bytes(const gdr::LinProblem &p);
 cudaError_t gdr_launch_linear(gdr::LinProblem &p, void *ws, cudaStream_t s, std::string *err);
 
-// y[b,t,hk,:] = sum over the group's heads of x[b,t,hk * G + i,:], for the tokens of the packed
-// sequences (all tokens when cu is null).
-cudaError_t gdr_launch_linear_group_sum(const float *x, void *y, bool bf16, int B, int T, int Hk, int G, int d,
-                                        const int *cu, int N, cudaStream_t s);
+// y[b,t,hk,:] = sum over the group's p.H / Hk heads of x[b,t,hk * G + i,:], for the tokens of the packed
+// sequences (all tokens when p.cu is null; zeros in the other rows when p.zero_rest).
+cudaError_t gdr_launch_linear_group_sum(const float *x, void *y, const gdr::LinProblem &p, int Hk, int d, cudaStream_t s);
 
 namespace gdr {
 struct LinDecodeProblem {

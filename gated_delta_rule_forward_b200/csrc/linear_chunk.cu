@@ -303,7 +303,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const LinRun &r = p.run[ri];
   if (warp == W_COPY && lane < 3) prefetch_tmap(&maps.m[lane == 0 ? r.ib : lane == 1 ? r.ic : r.ia]);
   const bool rev = r.reverse != 0;
+  const bool zero_rest = !PHASE1 && !YF32 && p.zero_rest;
+  int rest_first = 0, rest_end = p.T;
+  if (zero_rest) rest_first = lin_cu(p, 0), rest_end = lin_cu(p, p.N);
   const LinItem it = lin_item(p, blockIdx.x / sel.n);
+  if (zero_rest) lin_zero_rest(p, r.y, static_cast<size_t>(p.H) * DC * 2, rest_first, rest_end, blockIdx.x / sel.n, gridDim.x / sel.n);
   const int h = it.h;
   const bool last = rev ? it.g == 0 : it.g == it.nseg - 1;   // in the run's order
   if (!it.ok || (PHASE1 && last && (it.nseg == 1 || !r.s_final))) {

@@ -43,6 +43,8 @@ __global__ void __launch_bounds__(DC * 8 / NC) linear_token_kernel(const __grid_
   tc::griddep_launch_dependents();
   const LinRun &r = p.run[ir];
   const int tid = threadIdx.x, lane = tid & 31;
+  if (!PHASE1 && p.zero_rest && !r.y_f32)
+    lin_zero_rest(p, r.y, static_cast<size_t>(p.H) * DC * 4, lin_cu(p, 0), lin_cu(p, p.N), blockIdx.x, gridDim.x);
   const LinItem it = lin_item(p, blockIdx.x);
   const int h = it.h;
   const bool rev = r.reverse != 0;

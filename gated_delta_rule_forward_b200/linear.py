@@ -146,7 +146,8 @@ def linear_forward(q, k, v, *, log_decay, initial_state=None, output_final_state
     where, handle = _on(dev, stream)
     with where:
         if out is None:
-            out = (torch.empty if cu_seqlens is None else torch.zeros)(B, T, H, dv, device=dev, dtype=q.dtype)
+            out = (torch.empty if N else torch.zeros)(B, T, H, dv, device=dev, dtype=q.dtype)
+            a.zero_rest = 1
         if final_state is None and output_final_state:
             final_state = torch.empty(N, H, dk, dv, device=dev, dtype=f32)
         a.o = out.data_ptr()
@@ -182,7 +183,8 @@ def linear_backward(q, k, v, d_o, *, log_decay, initial_state=None, d_final_stat
         g.d_final_state = d_final_state.data_ptr()
     where, handle = _on(dev, stream)
     with where:
-        new = torch.empty if cu_seqlens is None and v.shape[2] else torch.zeros   # no value heads: sums of nothing
+        new = torch.empty if N and H else torch.zeros   # no value heads: sums of nothing
+        a.zero_rest = 1
         grads = {"q": new(B, T, Hk, dk, device=dev, dtype=q.dtype), "k": new(B, T, Hk, dk, device=dev, dtype=q.dtype),
                  "v": new(B, T, H, dv, device=dev, dtype=q.dtype),
                  "initial_state": torch.empty(N, H, dk, dv, device=dev, dtype=f32)}

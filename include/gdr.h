@@ -303,7 +303,7 @@ gdr_status_t gdr_backward(int variant, int dtype, int B, int T, int H, int dk, i
  *  - a packed batch: cu_seqlens (device, int32, N + 1 non-decreasing offsets
  *    from 0 to at most T) cuts the T tokens of one row (B = 1) into N
  *    sequences, which may be empty; rows behind the last sequence are not
- *    written.  Offsets outside [0, T] are taken as 0 or T.  Without
+ *    written, or (zero_rest) become zeros.  Offsets outside [0, T] are taken as 0 or T.  Without
  *    cu_seqlens N = B;
  *  - state_slots (device, int32, N) makes initial_state and final_state pools
  *    of `pages` states, sequence n's in page state_slots[n].  A slot outside
@@ -324,6 +324,7 @@ typedef struct {
     const int *cu_seqlens;       /* [N+1] or NULL */
     const int *state_slots;      /* [N] or NULL (state n) */
     int pages;                   /* pages of the state pools; used with state_slots */
+    int zero_rest;               /* nonzero: the outputs' rows of no packed sequence become zeros */
     const float *initial_state;  /* [N,H,dk,dv] or [pages,H,dk,dv], or NULL for zeros */
     float *final_state;          /* as initial_state, or NULL; may be the same buffer */
     void *o;                     /* [B,T,H,dv] I/O dtype (forward only) */

@@ -602,6 +602,35 @@ def test_padding_rows_with_any_contents():
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("Hk,H,dk,dv", [(2, 2, 128, 64), (1, 3, 64, 128), (1, 1, 64, 64)])
+@pytest.mark.parametrize("T,lens", [(400, [70, 0, 130]), (400, [0, 0]), (2500, [1400, 3, 0]), (700, [1]), (90, [64, 26])])
+def test_rows_of_no_sequence(dtype, Hk, H, dk, dv, T, lens):
+    """They are zeros in fresh outputs, whatever the memory held, and left as they were in a given one."""
+    q, k, v, g = tensors(51, 1, T, Hk, H, dk, dv, dtype)
+    do, ld = randn(g, 1, T, H, dv, dtype=dtype), decays(H)
+    cu = torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32)
+    used = sum(lens)
+    for x in (q, k, v, do):
+        x[:, used:] = float("nan")
+    held = [torch.full((T * H * d * 4,), float("nan"), device="cuda") for d in (64, 128, 64, 128)]
+    del held                                           # what the fresh outputs are made of
+    o, S = gdr.linear_forward(q, k, v, log_decay=ld, cu_seqlens=cu)
+    x = gdr.linear_backward(q, k, v, do, log_decay=ld, cu_seqlens=cu, d_final_state=torch.ones_like(S))
+    given = torch.full_like(v, 5.0)
+    gdr.linear_forward(q, k, v, log_decay=ld, cu_seqlens=cu, out=given)
+    fine()
+    assert torch.equal(given[:, :used], o[:, :used]) and (given[:, used:] == 5).all()
+    for name, y in (("o", o), ("q", x["q"]), ("k", x["k"]), ("v", x["v"])):
+        assert (y[:, used:] == 0).all() and torch.isfinite(y).all(), name
+    for n, L in enumerate(lens):
+        s = slice(sum(lens[:n]), sum(lens[:n]) + L)
+        if L <= 130:
+            ref.check_forward(q[0, s], k[0, s], v[0, s], ld, None, 1.0, o[0, s], S[n], f"sequence {n}")
+            ref.check_grads(q[0, s], k[0, s], v[0, s], do[0, s], ld, None, torch.ones_like(S[n]), 1.0,
+                            [x["q"][0, s], x["k"][0, s], x["v"][0, s], x["initial_state"][n]], f"sequence {n}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_changing_decays_and_offsets(dtype):
     """Decays, offsets and slots overwritten on the stream between two calls are the second call's."""
     lens = [[300, 1, 600], [2, 800, 99]]
