@@ -199,7 +199,7 @@ static size_t run_floats(const gdr::LinProblem &p, int i) {
 }
 size_t gdr_linear_workspace_bytes(const gdr::LinProblem &p) {
   size_t floats = 0;
-  for (int i = 0; i < p.nrun; ++i) floats += run_floats(p, i) * (p.G <= gdr::kLinSelfChain ? 2 : 1);
+  for (int i = 0; i < p.nrun; ++i) floats += run_floats(p, i) * (gdr::lin_self_chains(p) ? 2 : 1);
   return floats * sizeof(float);
 }
 
@@ -208,7 +208,7 @@ cudaError_t gdr_launch_linear(gdr::LinProblem &p, void *ws, cudaStream_t s, std:
   for (int i = 0; i < p.nrun; ++i) {
     p.run[i].X = X;
     X += run_floats(p, i);
-    if (p.G > gdr::kLinSelfChain) continue;
+    if (!gdr::lin_self_chains(p)) continue;
     p.run[i].XS = X;
     X += run_floats(p, i);
   }
@@ -222,7 +222,7 @@ cudaError_t gdr_launch_linear(gdr::LinProblem &p, void *ws, cudaStream_t s, std:
   cudaError_t e;
   // (an end state in the place of its start state is written by the chain kernel: phase 2's segments
   // read the start state side by side)
-  p.chained = segmented && p.G > gdr::kLinSelfChain;
+  p.chained = segmented && !gdr::lin_self_chains(p);
   for (int i = 0; i < p.nrun; ++i) p.chained |= segmented && p.run[i].s0 && p.run[i].s0 == p.run[i].s_final;
   if (segmented) {
     if ((e = phase(true, false)) != cudaSuccess) return *err = "segment states: ", e;

@@ -70,8 +70,14 @@ struct LinProblem {
 // A run's blocks are its segments of every head; each has a state in X.
 inline long lin_blocks(const LinProblem &p) { return static_cast<long>(p.items) * p.H; }
 inline bool lin_segmented(const LinProblem &p) { return p.G > 1; }
-// Segments up to which phase 2 chains the states itself.
-constexpr int kLinSelfChain = 4;
+// Segments up to which phase 2 chains the states itself.  In a packed bf16 forward whose sequences have one on
+// average G is only a bound, and those that run whole then start beside phase 1, as they do not behind a chain
+// kernel: 16 ragged prompts of 9200 tokens, 16 heads, 69 us for 75, of 128 x 128 71 for 82.  (Two sequences in five
+// segments each: 66 for 61; the packed backward 286 for 283, fp32 527 for 519.)
+constexpr int kLinSelfChain = 4, kLinSelfChainPacked = 16;
+inline bool lin_self_chains(const LinProblem &p) {
+  return p.G <= kLinSelfChain || (p.G <= kLinSelfChainPacked && p.cu && p.bf16_io && p.nrun == 1 && p.N >= p.G);
+}
 
 #ifdef __CUDACC__
 // One segment of one (sequence, head).  `ok` is false for an index past the last one.
@@ -205,6 +211,46 @@ __device__ __forceinline__ void lin_self_chain(const LinProblem &p, const LinRun
       s.w = fmaf(f[k], s.w, d[k].w);
     }
     if (fin) *reinterpret_cast<float4 *>(r.s_final + at_page + e) = s;
+  }
+}
+
+// The same for any number of segments of a forward, their loads four at a time.
+__device__ __forceinline__ void lin_self_chain_long(const LinProblem &p, const LinRun &r, const LinItem &it, int page,
+                                                    bool last, int da, int dc, float *to, int tid, int threads) {
+  const float ld = __ldg(p.log_decay + it.h);
+  const size_t elems = static_cast<size_t>(da) * dc;
+  const float *X = r.X + static_cast<size_t>(it.slot - it.g * it.step) * elems;   // segment 0's
+  const bool fin = last && r.s_final && page >= 0;
+  const size_t at_page = (static_cast<size_t>(page < 0 ? 0 : page) * p.H + it.h) * elems;
+  const int steps = it.g + fin;
+  float full, ftail;   // the decays over a segment and over the sequence's last one, each computed by a lane
+  {
+    const float x = lin_pow64(ld, tid & 1 ? it.len - (it.nseg - 1) * p.seg : p.seg);
+    full = __shfl_sync(0xffffffffu, x, 0);
+    ftail = __shfl_sync(0xffffffffu, x, 1);
+  }
+  constexpr int U = 4;
+  for (int e = 4 * tid; e < static_cast<int>(elems); e += 4 * threads) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r.s0 && page >= 0) s = *reinterpret_cast<const float4 *>(r.s0 + at_page + e);
+#pragma unroll 1
+    for (int k0 = 0; k0 < steps; k0 += U) {
+      float4 d[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (k0 + k < steps) d[k] = *reinterpret_cast<const float4 *>(X + static_cast<size_t>(k0 + k) * it.step * elems + e);
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        if (k0 + k >= steps) break;
+        if (k0 + k == it.g) *reinterpret_cast<float4 *>(to + e) = s;
+        const float f = k0 + k == it.nseg - 1 ? ftail : full;
+        s.x = fmaf(f, s.x, d[k].x);
+        s.y = fmaf(f, s.y, d[k].y);
+        s.z = fmaf(f, s.z, d[k].z);
+        s.w = fmaf(f, s.w, d[k].w);
+      }
+    }
+    *reinterpret_cast<float4 *>(fin ? r.s_final + at_page + e : to + e) = s;
   }
 }
 

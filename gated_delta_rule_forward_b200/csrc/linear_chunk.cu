@@ -291,7 +291,8 @@ __device__ __forceinline__ void split_pair(uint32_t x, float w0, float w1, uint3
 }
 
 // YF32: y in fp32 (the value heads' shares of a shared head's gradient).
-template <int DA, int DC, bool PHASE1, bool YF32>
+// LONG: phase 2 chains any number of segments (kLinSelfChain otherwise), whose code costs the others registers.
+template <int DA, int DC, bool PHASE1, bool YF32, bool LONG>
 __global__ void __launch_bounds__(NTHREADS, 1)
     linear_chunk_kernel(const __grid_constant__ LinProblem p, const __grid_constant__ LinChunkMaps maps,
                         const LinRunSel sel) {
@@ -405,7 +406,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   griddep_launch_dependents();
   if (!PHASE1 && it.nseg > 1 && !p.chained) {
     float *mine = r.XS + static_cast<size_t>(it.slot) * DA * DC;
-    lin_self_chain(p, r, it, page, last, DA, DC, mine, tid, NTHREADS);
+    if (LONG) lin_self_chain_long(p, r, it, page, last, DA, DC, mine, tid, NTHREADS);
+    else lin_self_chain(p, r, it, page, last, DA, DC, mine, tid, NTHREADS);
     start = mine;
     __syncthreads();
   }
@@ -837,10 +839,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
 }
 
-template <int DA, int DC, bool PHASE1, bool YF32>
+template <int DA, int DC, bool PHASE1, bool YF32, bool LONG>
 cudaError_t launch(const LinProblem &p, const LinChunkMaps &maps, const LinRunSel &sel, bool pdl, cudaStream_t s) {
   constexpr uint32_t SMEM = Smem<PHASE1>::BYTES;
-  auto kern = linear_chunk_kernel<DA, DC, PHASE1, YF32>;
+  auto kern = linear_chunk_kernel<DA, DC, PHASE1, YF32, LONG>;
   // the kernel's limit on the current device, set by the first call there
   static std::atomic<unsigned long long> set{0};
   int dev = 0;
@@ -864,13 +866,13 @@ cudaError_t launch(const LinProblem &p, const LinChunkMaps &maps, const LinRunSe
   return cudaLaunchKernelEx(&cfg, kern, p, maps, sel);
 }
 
-template <bool PHASE1, bool YF32>
+template <bool PHASE1, bool YF32, bool LONG>
 cudaError_t launch_shape(int da, int dc, const LinProblem &p, const LinChunkMaps &m, const LinRunSel &sel, bool pdl,
                          cudaStream_t s) {
-  if (da == 128 && dc == 128) return launch<128, 128, PHASE1, YF32>(p, m, sel, pdl, s);
-  if (da == 128 && dc == 64) return launch<128, 64, PHASE1, YF32>(p, m, sel, pdl, s);
-  if (da == 64 && dc == 128) return launch<64, 128, PHASE1, YF32>(p, m, sel, pdl, s);
-  return launch<64, 64, PHASE1, YF32>(p, m, sel, pdl, s);
+  if (da == 128 && dc == 128) return launch<128, 128, PHASE1, YF32, LONG>(p, m, sel, pdl, s);
+  if (da == 128 && dc == 64) return launch<128, 64, PHASE1, YF32, LONG>(p, m, sel, pdl, s);
+  if (da == 64 && dc == 128) return launch<64, 128, PHASE1, YF32, LONG>(p, m, sel, pdl, s);
+  return launch<64, 64, PHASE1, YF32, LONG>(p, m, sel, pdl, s);
 }
 
 }  // namespace
@@ -924,9 +926,11 @@ cudaError_t gdr_launch_linear_chunk(const gdr::LinProblem &p, const gdr::LinChun
     // wait, run beside it and end after it
     sel.beside = i > 0;
     const bool dep = pdl || sel.beside;
-    const cudaError_t e = phase1    ? gdr::tc::launch_shape<true, false>(a.da, a.dc, p, maps, sel, dep, s)
-                          : a.y_f32 ? gdr::tc::launch_shape<false, true>(a.da, a.dc, p, maps, sel, dep, s)
-                                    : gdr::tc::launch_shape<false, false>(a.da, a.dc, p, maps, sel, dep, s);
+    const bool longer = !p.chained && p.G > gdr::kLinSelfChain;   // (a forward: no y_f32)
+    const cudaError_t e = phase1    ? gdr::tc::launch_shape<true, false, false>(a.da, a.dc, p, maps, sel, dep, s)
+                          : a.y_f32 ? gdr::tc::launch_shape<false, true, false>(a.da, a.dc, p, maps, sel, dep, s)
+                          : longer  ? gdr::tc::launch_shape<false, false, true>(a.da, a.dc, p, maps, sel, dep, s)
+                                    : gdr::tc::launch_shape<false, false, false>(a.da, a.dc, p, maps, sel, dep, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -601,6 +601,36 @@ def test_padding_rows_with_any_contents():
     assert torch.equal(pool[0], before[0]) and torch.equal(pool[1:], one)
 
 
+# (256 tokens a segment: up to six of them in a sequence, at most 10 and 12 in a batch of 12 sequences)
+@pytest.mark.parametrize("Hk,H,dk,dv,state", [(1, 2, 128, 64, True), (1, 1, 64, 128, True), (2, 2, 64, 64, False),
+                                              (1, 1, 128, 128, True)])
+@pytest.mark.parametrize("lens", [[3, 1500, 0, 1, 70, 256, 0, 64, 2, 130, 513, 9], [0] * 11 + [1281], [1024, 1025] + [40] * 10])
+def test_packed_long_among_short(Hk, H, dk, dv, state, lens):
+    N, T = len(lens), sum(lens) + 5
+    q, k, v, g = tensors(61, 1, T, Hk, H, dk, dv, BF16)
+    pages, ld = N + 2, torch.tensor([-0.004, -0.5], device="cuda")[:H].contiguous()
+    slots = torch.randperm(pages, generator=g, device="cuda")[:N].to(torch.int32)
+    S0 = randn(g, pages, H, dk, dv) if state else None
+    cu = torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32)
+    S, place = torch.full((pages, H, dk, dv), 7.0, device="cuda"), torch.zeros(pages, H, dk, dv, device="cuda")
+    if state:
+        place.copy_(S0)
+    o, _ = gdr.linear_forward(q, k, v, log_decay=ld, initial_state=S0, final_state=S, state_slots=slots, cu_seqlens=cu)
+    none, _ = gdr.linear_forward(q, k, v, log_decay=ld, initial_state=S0, state_slots=slots if state else None, cu_seqlens=cu,
+                                 output_final_state=False)
+    there, _ = gdr.linear_forward(q, k, v, log_decay=ld, initial_state=place, final_state=place, state_slots=slots,
+                                  cu_seqlens=cu)
+    fine()
+    assert (S[[p for p in range(pages) if p not in slots.tolist()]] == 7).all()
+    at = slots.tolist()
+    assert torch.equal(o, there) and torch.equal(S[at], place[at])
+    for n, p in enumerate(at):
+        s = slice(sum(lens[:n]), sum(lens[:n + 1]))
+        ref.check_forward(q[0, s], k[0, s], v[0, s], ld, S0[p] if state else None, 1.0, o[0, s], S[p], f"sequence {n}")
+        # (a state that is not kept takes two bf16 terms of w c instead of three: other bits, the same bound)
+        ref.check_forward(q[0, s], k[0, s], v[0, s], ld, S0[p] if state else None, 1.0, none[0, s], None, f"no state {n}")
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("Hk,H,dk,dv", [(2, 2, 128, 64), (1, 3, 64, 128), (1, 1, 64, 64)])
 @pytest.mark.parametrize("T,lens", [(400, [70, 0, 130]), (400, [0, 0]), (2500, [1400, 3, 0]), (700, [1]), (90, [64, 26])])
