@@ -220,10 +220,14 @@ cudaError_t gdr_launch_linear(gdr::LinProblem &p, void *ws, cudaStream_t s, std:
     return chunk ? gdr_launch_linear_chunk(p, maps, phase1, pdl, s) : gdr_launch_linear_token(p, phase1, pdl, s);
   };
   cudaError_t e;
-  // (an end state in the place of its start state is written by the chain kernel: phase 2's segments
-  // read the start state side by side)
+  // (phase 2's segments read the start state side by side: an end state in its place is written by the chain kernel, or
+  // in a packed forward they read phase 1's copy of it)
   p.chained = segmented && !gdr::lin_self_chains(p);
-  for (int i = 0; i < p.nrun; ++i) p.chained |= segmented && p.run[i].s0 && p.run[i].s0 == p.run[i].s_final;
+  for (int i = 0; i < p.nrun; ++i)
+    if (segmented && p.run[i].s0 && p.run[i].s0 == p.run[i].s_final) {
+      p.s0_copied = !p.chained && chunk && p.cu && p.nrun == 1;
+      p.chained |= !p.s0_copied;
+    }
   if (segmented) {
     if ((e = phase(true, false)) != cudaSuccess) return *err = "segment states: ", e;
     if (p.chained && (e = gdr_launch_linear_chain(p, true, s)) != cudaSuccess) return *err = "segment chain: ", e;

@@ -64,6 +64,7 @@ struct LinProblem {
   int G;                 // segments of a sequence (packed: at most)
   int items;             // (sequence, segment) pairs (packed: an upper bound)
   int chained;           // X holds start states already (the chain kernel ran)
+  int s0_copied;         // phase 1 leaves the sequences' start states in their first segments' XS (a packed forward in place)
   int zero_rest;         // the outputs' rows of no packed sequence become zeros
 };
 
@@ -214,7 +215,8 @@ __device__ __forceinline__ void lin_self_chain(const LinProblem &p, const LinRun
   }
 }
 
-// The same for any number of segments of a forward, their loads four at a time.
+// The same for any number of segments of a forward, their loads four at a time.  (With a copied start state the
+// first segment's is there already.)
 __device__ __forceinline__ void lin_self_chain_long(const LinProblem &p, const LinRun &r, const LinItem &it, int page,
                                                     bool last, int da, int dc, float *to, int tid, int threads) {
   const float ld = __ldg(p.log_decay + it.h);
@@ -223,6 +225,10 @@ __device__ __forceinline__ void lin_self_chain_long(const LinProblem &p, const L
   const bool fin = last && r.s_final && page >= 0;
   const size_t at_page = (static_cast<size_t>(page < 0 ? 0 : page) * p.H + it.h) * elems;
   const int steps = it.g + fin;
+  if (p.s0_copied && it.g == 0) return;
+  const float *s0 = p.s0_copied           ? r.XS + static_cast<size_t>(it.slot - it.g * it.step) * elems
+                    : r.s0 && page >= 0 ? r.s0 + at_page
+                                        : nullptr;
   float full, ftail;   // the decays over a segment and over the sequence's last one, each computed by a lane
   {
     const float x = lin_pow64(ld, tid & 1 ? it.len - (it.nseg - 1) * p.seg : p.seg);
@@ -232,7 +238,7 @@ __device__ __forceinline__ void lin_self_chain_long(const LinProblem &p, const L
   constexpr int U = 4;
   for (int e = 4 * tid; e < static_cast<int>(elems); e += 4 * threads) {
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r.s0 && page >= 0) s = *reinterpret_cast<const float4 *>(r.s0 + at_page + e);
+    if (s0) s = *reinterpret_cast<const float4 *>(s0 + e);
 #pragma unroll 1
     for (int k0 = 0; k0 < steps; k0 += U) {
       float4 d[U];

@@ -291,7 +291,8 @@ __device__ __forceinline__ void split_pair(uint32_t x, float w0, float w1, uint3
 }
 
 // YF32: y in fp32 (the value heads' shares of a shared head's gradient).
-// LONG: phase 2 chains any number of segments (kLinSelfChain otherwise), whose code costs the others registers.
+// LONG: phase 2 chains any number of segments (kLinSelfChain otherwise) or from copied start states, whose code costs
+// the others registers.
 template <int DA, int DC, bool PHASE1, bool YF32, bool LONG>
 __global__ void __launch_bounds__(NTHREADS, 1)
     linear_chunk_kernel(const __grid_constant__ LinProblem p, const __grid_constant__ LinChunkMaps maps,
@@ -404,6 +405,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const float *start = r.X + static_cast<size_t>(it.slot) * DA * DC;
   if (!sel.beside && (PHASE1 || it.nseg > 1)) griddep_wait();
   griddep_launch_dependents();
+  if (PHASE1 && p.s0_copied && it.g == 0) {
+    const float4 *src = reinterpret_cast<const float4 *>(r.s0 + (static_cast<size_t>(max(page, 0)) * p.H + h) * DA * DC);
+    float4 *dst = reinterpret_cast<float4 *>(r.XS + static_cast<size_t>(it.slot) * DA * DC);
+    for (int e = tid; e < DA * DC / 4; e += NTHREADS) dst[e] = page >= 0 ? src[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   if (!PHASE1 && it.nseg > 1 && !p.chained) {
     float *mine = r.XS + static_cast<size_t>(it.slot) * DA * DC;
     if (LONG) lin_self_chain_long(p, r, it, page, last, DA, DC, mine, tid, NTHREADS);
@@ -926,7 +932,7 @@ cudaError_t gdr_launch_linear_chunk(const gdr::LinProblem &p, const gdr::LinChun
     // wait, run beside it and end after it
     sel.beside = i > 0;
     const bool dep = pdl || sel.beside;
-    const bool longer = !p.chained && p.G > gdr::kLinSelfChain;   // (a forward: no y_f32)
+    const bool longer = !p.chained && (p.G > gdr::kLinSelfChain || p.s0_copied);   // (a forward: no y_f32)
     const cudaError_t e = phase1    ? gdr::tc::launch_shape<true, false, false>(a.da, a.dc, p, maps, sel, dep, s)
                           : a.y_f32 ? gdr::tc::launch_shape<false, true, false>(a.da, a.dc, p, maps, sel, dep, s)
                           : longer  ? gdr::tc::launch_shape<false, false, true>(a.da, a.dc, p, maps, sel, dep, s)

@@ -604,7 +604,8 @@ def test_padding_rows_with_any_contents():
 # (256 tokens a segment: up to six of them in a sequence, at most 10 and 12 in a batch of 12 sequences)
 @pytest.mark.parametrize("Hk,H,dk,dv,state", [(1, 2, 128, 64, True), (1, 1, 64, 128, True), (2, 2, 64, 64, False),
                                               (1, 1, 128, 128, True)])
-@pytest.mark.parametrize("lens", [[3, 1500, 0, 1, 70, 256, 0, 64, 2, 130, 513, 9], [0] * 11 + [1281], [1024, 1025] + [40] * 10])
+@pytest.mark.parametrize("lens", [[3, 1500, 0, 1, 70, 256, 0, 64, 2, 130, 513, 9], [0] * 11 + [1281], [1024, 1025] + [40] * 10,
+                                  [3, 700, 130], [513]])
 def test_packed_long_among_short(Hk, H, dk, dv, state, lens):
     N, T = len(lens), sum(lens) + 5
     q, k, v, g = tensors(61, 1, T, Hk, H, dk, dv, BF16)
@@ -620,7 +621,17 @@ def test_packed_long_among_short(Hk, H, dk, dv, state, lens):
                                  output_final_state=False)
     there, _ = gdr.linear_forward(q, k, v, log_decay=ld, initial_state=place, final_state=place, state_slots=slots,
                                   cu_seqlens=cu)
+    # the longest sequence without a page: zeros at its start, and no state of it kept
+    longest = lens.index(max(lens))
+    outside, pool = slots.clone(), randn(g, pages, H, dk, dv)
+    outside[longest] = pages
+    before = pool.clone()
+    lost, _ = gdr.linear_forward(q, k, v, log_decay=ld, initial_state=pool, final_state=pool, state_slots=outside,
+                                 cu_seqlens=cu)
     fine()
+    assert torch.equal(pool[slots[longest]], before[slots[longest]])
+    s = slice(sum(lens[:longest]), sum(lens[:longest + 1]))
+    ref.check_forward(q[0, s], k[0, s], v[0, s], ld, None, 1.0, lost[0, s], None, "without a page")
     assert (S[[p for p in range(pages) if p not in slots.tolist()]] == 7).all()
     at = slots.tolist()
     assert torch.equal(o, there) and torch.equal(S[at], place[at])
