@@ -260,14 +260,27 @@ __device__ __forceinline__ void lin_self_chain_long(const LinProblem &p, const L
   }
 }
 
-// exp(n * log_decay), the product's rounding error carried into the result;
-// lambda^0 = 1 for every decay, -inf included.
-__device__ __forceinline__ float lin_pow(float log_decay, int n) {
-  if (n == 0) return 1.f;
-  const float x = log_decay * static_cast<float>(n);
-  if (!(x > -200.f)) return x <= -200.f ? 0.f : x;   // zero in fp32; NaN stays
-  const float e = fmaf(log_decay, static_cast<float>(n), -x);
-  return expf(x) * (1.f + e);
+// lambda as hi + lo, off by a few roundings (2^-24) of the smaller of lambda and 1 - lambda: above 1/2 from
+// e = lambda - 1 = t (t + 2), t = exp(x) - 1 at half the decay by its Taylor series to x^8 (|x| < 0.35: the
+// next term is 6e-10 of it).  lo is above zero where lambda is, so that an infinite state stays one.  In every
+// thread and without a branch: with expm1f, or in one warp for all, decoding 256 rows of 16 heads of
+// 64 x 64 takes 16.4 and 15.8 us for 15.4, with one fp32 lambda 15.2.
+__device__ __forceinline__ float2 lin_decay(float log_decay) {
+  const float x = 0.5f * log_decay;
+  float e = 1.f / 40320.f;
+  e = fmaf(e, x, 1.f / 5040.f);
+  e = fmaf(e, x, 1.f / 720.f);
+  e = fmaf(e, x, 1.f / 120.f);
+  e = fmaf(e, x, 1.f / 24.f);
+  e = fmaf(e, x, 1.f / 6.f);
+  e = fmaf(e, x, 0.5f);
+  e = fmaf(e * x, x, x);
+  e = fmaf(e, e, 2.f * e);
+  const float near = __fadd_rd(1.f, e);   // and e - (near - 1): both differences exact
+  const bool small = log_decay > -0.6931472f;
+  const float hi = small ? near : expf(log_decay);
+  const float lo = small ? e - (near - 1.f) : 0.f;
+  return make_float2(hi, fmaxf(lo, hi * 0x1p-60f));
 }
 #endif
 

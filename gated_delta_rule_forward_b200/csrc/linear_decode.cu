@@ -4,6 +4,11 @@
 //
 //     S <- lambda S + k v^T,   o = scale S^T q
 //
+// The same lambda multiplies a state for thousands of steps, so its error compounds over
+// the state's memory of 1 / (1 - lambda) of them: one fp32 value of it is off by up to
+// 2^-25, which a decay of -1e-6 makes 3%.  It is taken as hi + lo (lin_decay):
+//     S <- hi S + (lo S + k v^T).
+//
 // The value columns are independent, so a (row, head) may be cut into slices of
 // columns, one CTA of 256 threads each: thread (rg, cq) holds columns
 // 4 cq .. 4 cq + 3 of rows rg, rg + RG, ..., with all its float4 loads issued
@@ -48,18 +53,19 @@ __global__ void __launch_bounds__(kThreads) linear_decode_kernel(const LinDecode
   float v[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) v[c] = ld_io<IO>(static_cast<const IO *>(p.v) + nh * p.dv + sl * W + 4 * cq + c);
-  const float lam = lin_pow(__ldg(p.log_decay + h), 1);
+  const float2 lam = lin_decay(__ldg(p.log_decay + h));
   __syncthreads();
+  auto update = [&](float s, float kv) { return fmaf(lam.x, s, fmaf(lam.y, s, kv)); };
 
   float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int r = 0; r < RPT; ++r) {
     const int i = rg + RG * r;
     const float k = kf[i], q = qf[i];
-    s[r].x = fmaf(lam, s[r].x, k * v[0]);
-    s[r].y = fmaf(lam, s[r].y, k * v[1]);
-    s[r].z = fmaf(lam, s[r].z, k * v[2]);
-    s[r].w = fmaf(lam, s[r].w, k * v[3]);
+    s[r].x = update(s[r].x, k * v[0]);
+    s[r].y = update(s[r].y, k * v[1]);
+    s[r].z = update(s[r].z, k * v[2]);
+    s[r].w = update(s[r].w, k * v[3]);
     *reinterpret_cast<float4 *>(S + static_cast<size_t>(i) * p.dv) = s[r];
     y[0] = fmaf(s[r].x, q, y[0]);
     y[1] = fmaf(s[r].y, q, y[1]);
