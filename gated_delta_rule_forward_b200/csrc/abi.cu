@@ -25,10 +25,11 @@ gdr_status_t fail(gdr_status_t st, const std::string &why) {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-bool injected_launch_fault() {
+bool injected_fault(const char *kind) {
   const char *f = std::getenv("GDR_FAULT");
-  return f && std::strcmp(f, "launch") == 0;
+  return f && std::strcmp(f, kind) == 0;
 }
+bool injected_launch_fault() { return injected_fault("launch"); }
 
 gdr_status_t check_cuda(cudaError_t e, const char *what) {
   if (e == cudaSuccess) return GDR_OK;
@@ -526,6 +527,7 @@ gdr_status_t gdr_linear_forward(int dtype, int B, int T, int Hk, int H, int dk, 
   if (injected_launch_fault()) return fail(GDR_ERR_CUDA, "injected launch failure (GDR_FAULT=launch)");
   p.cu = a->cu_seqlens; p.slots = a->state_slots; p.pages = a->state_slots ? a->pages : N;
   p.zero_rest = a->cu_seqlens && a->zero_rest;
+  p.fault = injected_fault("wait");
   p.log_decay = a->log_decay;
   gdr::LinRun &r = p.run[0];
   r.yscale = scale; r.y = a->o; r.s0 = a->initial_state; r.s_final = a->final_state;
@@ -570,6 +572,7 @@ gdr_status_t gdr_linear_backward(int dtype, int B, int T, int Hk, int H, int dk,
   if (injected_launch_fault()) return fail(GDR_ERR_CUDA, "injected launch failure (GDR_FAULT=launch)");
   p.cu = a->cu_seqlens; p.pages = N;
   p.zero_rest = a->cu_seqlens && a->zero_rest;
+  p.fault = injected_fault("wait");
   p.log_decay = a->log_decay;
   float *dq32 = nullptr, *dk32 = nullptr;
   if (H != Hk && T > 0) {

@@ -66,6 +66,7 @@ struct LinProblem {
   int chained;           // X holds start states already (the chain kernel ran)
   int s0_copied;         // phase 1 leaves the sequences' start states in their first segments' XS (a packed forward in place)
   int zero_rest;         // the outputs' rows of no packed sequence become zeros
+  int fault;             // the bf16 kernels' first block leaves out what its waits wait for (failure tests)
 };
 
 // A run's blocks are its segments of every head; each has a state in X.

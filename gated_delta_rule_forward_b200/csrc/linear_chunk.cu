@@ -101,7 +101,8 @@ struct Smem {
   static constexpr uint32_t SOP = DS + 16;           // S^T of the chunk's start in tensor memory (8 warps)
   static constexpr uint32_t DRAIN = SOP + 8;
   static constexpr uint32_t PTAIL = DRAIN + 24;      // P of the short chunk formed (once)
-  static constexpr uint32_t SLOT = PTAIL + 8;        // tensor-memory address
+  static constexpr uint32_t CREAD = PTAIL + 8;       // c of the short chunk read (8 warps, once)
+  static constexpr uint32_t SLOT = CREAD + 8;        // tensor-memory address
   static constexpr uint32_t ABORT = SLOT + 4;        // a wait gave up
   static constexpr uint32_t BYTES = ABORT + 4 + 1024;
   static_assert(BAR % 16 == 0 && P % 1024 == 0 && BYTES <= 232448, "one CTA per SM");
@@ -328,6 +329,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tmem_alloc(reinterpret_cast<uint32_t *>(sm + M::SLOT), TMEM_COLS);
     tmem_relinquish();
   }
+  // host fault injection: the first block copies no first chunk (phase 1), or forms no P, so that its waits run out
+  const bool faulty = p.fault && blockIdx.x == 0;
   const int beg = it.beg, end = it.end;
   const int nch = __shfl_sync(0xffffffffu, (end - beg + C - 1) / C, 0);
   // copies of one chunk into its stage, and of the chunk that comes there next as far as L2
@@ -370,10 +373,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     init(M::SOP, 1, NSTATE);
     init(M::DRAIN, 3, 1);
     init(M::PTAIL, 1, 1);
+    init(M::CREAD, 1, NPREP);
     *reinterpret_cast<uint32_t *>(sm + M::ABORT) = 0;
     fence_mbar_init();
     // the first chunks: their tensors are inputs of the call, whatever grid this one depends on
-    for (int i = 0; i < NST && i < nch; ++i) copy_chunk(i, i);
+    for (int i = PHASE1 && faulty ? 1 : 0; i < NST && i < nch; ++i) copy_chunk(i, i);
   }
   if (tid >= 64 && tid < 64 + 65) {
     const int m = tid - 64;
@@ -429,7 +433,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         copy_chunk(i, st.at);
       }
       // nothing may land in shared memory after the CTA (each wait bounded)
-      for (int j = i > NST ? i - NST : 0; j < i; ++j)
+      for (int j = i > NST ? i - NST : PHASE1 && faulty ? 1 : 0; j < i; ++j)
         mbar_wait(reinterpret_cast<uint64_t *>(sm + M::LOAD) + j % NST, (j / NST) & 1);
     }
     if (sel.beside) griddep_wait();   // what follows this grid follows the one beside it
@@ -447,7 +451,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     Ring<NST> st;
     Ring<2> bf;
     if (warp == W_MMA_P) {   // P = a b^T, as soon as the chunk before's is read
-      for (int i = 0; !PHASE1 && i < nch; ++i, st.next(), bf.next()) {
+      for (int i = 0; !PHASE1 && !faulty && i < nch; ++i, st.next(), bf.next()) {
         if (i > 0 && !wait(M::PREAD, (i - 1) & 1)) break;
         if (!wait(M::LOAD + 8 * st.at, st.phase)) break;
         tc_fence_after();
@@ -493,10 +497,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         commit_one(base + M::FREE + 8 * st.at, e);
       }
     }
-    if (!ok) {   // a wait gave up: the MMAs in flight finish before the memory they use is released
-      commit_one(base + M::DRAIN + 8 * (warp - W_MMA_P), elect_one());
-      mbar_wait(reinterpret_cast<uint64_t *>(sm + M::DRAIN) + (warp - W_MMA_P), 0);
-    }
+    // the MMAs in flight finish before the memory they use is released, also where a wait gave up and nobody
+    // else waits for them
+    commit_one(base + M::DRAIN + 8 * (warp - W_MMA_P), elect_one());
+    mbar_wait(reinterpret_cast<uint64_t *>(sm + M::DRAIN) + (warp - W_MMA_P), 0);
   } else if (warp >= W_PREP) {
     // ---------------------------------------------------------------- prep: w c
     regs_dec<R_PREP>();
@@ -574,8 +578,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (n < C) {
         // rows behind the sequence's end, which the products read as well, become zeros (once all of c is
         // read and P is formed; the output warps clear P of them)
+        __syncwarp();
+        if (lane == 0) arrive_at(base + M::CREAD);
         if (!PHASE1 && !warp_wait_at(base + M::PTAIL, 0, abort)) break;
-        named_bar_sync(1, 32 * NPREP);
+        if (!warp_wait_at(base + M::CREAD, 0, abort)) break;
         uint8_t *sb = sm + M::STAGE * st.at;
         const int row = tid & 63, piece = (tid >> 6) & 3;
         if (row >= n) {
