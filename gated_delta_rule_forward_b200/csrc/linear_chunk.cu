@@ -555,6 +555,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const uint32_t zero[8] = {};
       for (int t = 0; t < (PHASE1 ? 8 : 4); ++t)   // every column of the buffers
         for (int g = 0; g < 2; ++g) tmem_st_frag4(wlane + (static_cast<uint32_t>(16 * g) << 16) + T::term(0, t), zero);
+      tmem_wait_st();   // here: an empty sequence has no chunk to wait in, and the CTA frees the memory at once
     }
     Ring<NST> st;
     Ring<2> bf;

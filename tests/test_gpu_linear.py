@@ -702,3 +702,22 @@ def test_changing_decays_and_offsets(dtype):
     fine()
     for i, x in got:
         assert all(torch.equal(a, b) for a, b in zip(x, want[i]))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_empty_sequences_of_narrow_values(dtype):
+    """Batches of nothing but empty sequences, each ending at once, right before one that computes."""
+    N, H, dk, dv = 700, 2, 128, 64
+    q, k, v, g = tensors(71, 1, 130, H, H, dk, dv, dtype)
+    S0, ld = randn(g, N, H, dk, dv), torch.tensor([-0.1, -0.01], device="cuda")
+    nothing = torch.zeros(N + 1, device="cuda", dtype=torch.int32)
+    dense = [gdr.linear_forward(q, k, v, log_decay=ld) for _ in range(2)]
+    for _ in range(5):
+        o, S = gdr.linear_forward(q, k, v, log_decay=ld, initial_state=S0, cu_seqlens=nothing)
+        dense.append(gdr.linear_forward(q, k, v, log_decay=ld))
+        x = gdr.linear_backward(q, k, v, v, log_decay=ld, d_final_state=S0, cu_seqlens=nothing)
+        assert torch.equal(S, S0) and (o == 0).all() and torch.equal(x["initial_state"], S0)
+        assert all((x[n] == 0).all() for n in "qkv")
+    fine()
+    assert all(torch.equal(a, b) for d in dense for a, b in zip(d, dense[0]))
+    ref.check_forward(q[0], k[0], v[0], ld, None, 1.0, dense[-1][0][0], dense[-1][1][0])
