@@ -470,8 +470,8 @@ static void linear_shape(gdr::LinProblem *p, int dtype, int B, int T, int H, int
   if (backward) {
     p->nrun = 3;
     p->run[0] = linear_run(3, 2, 1, dv, dk, 0, 1.f, 1.f, nullptr);   // dq = run(dO, v, k)
-    p->run[1] = linear_run(1, 0, 3, dk, dv, 1, 1.f, 1.f, nullptr);   // dv = reverse run(k, q, dO)
-    p->run[2] = linear_run(2, 3, 0, dv, dk, 1, 1.f, 1.f, nullptr);   // dk = reverse run(v, dO, q)
+    p->run[1] = linear_run(2, 3, 0, dv, dk, 1, 1.f, 1.f, nullptr);   // dk = reverse run(v, dO, q)
+    p->run[2] = linear_run(1, 0, 3, dk, dv, 1, 1.f, 1.f, nullptr);   // dv = reverse run(k, q, dO)
   } else {
     p->nrun = 1;
     p->run[0] = linear_run(0, 1, 2, dk, dv, 0, 1.f, 1.f, nullptr);   // o = run(q, k, v)
@@ -579,7 +579,7 @@ gdr_status_t gdr_linear_backward(int dtype, int B, int T, int Hk, int H, int dk,
     dq32 = reinterpret_cast<float *>(static_cast<char *>(workspace) + linear_state_bytes(p));
     dk32 = dq32 + static_cast<size_t>(B) * T * H * dk;
   }
-  gdr::LinRun &rq = p.run[0], &rv = p.run[1], &rk = p.run[2];
+  gdr::LinRun &rq = p.run[0], &rk = p.run[1], &rv = p.run[2];
   rq.yscale = scale; rq.s0 = a->initial_state; rq.s0_t = 1;
   rv.bscale = scale; rv.s0 = g->d_final_state; rv.s_final = g->d_initial_state;
   rk.bscale = scale; rk.s0 = g->d_final_state; rk.s0_t = 1;

@@ -145,6 +145,13 @@ __device__ __forceinline__ LinItem lin_item(const LinProblem &p, int block) {
   return it;
 }
 
+// The run a block of a phase's launch belongs to (one run's blocks come after another's).  As comparisons: with the
+// index as a quotient the bf16 backward of 4 sequences of 4096 tokens, 16 heads, takes 218 us for 208.
+__device__ __forceinline__ const LinRun &lin_run(const LinProblem &p) {
+  const unsigned blocks = gridDim.x / p.nrun;
+  return p.run[blockIdx.x < blocks ? 0 : blockIdx.x < 2 * blocks ? 1 : 2];
+}
+
 // This block's share of the zeros in a run's output rows of no sequence: [0, first) and [end, T), the offsets
 // cu[0] and cu[N].
 __device__ __forceinline__ void lin_zero_rest(const LinProblem &p, void *y, size_t row_bytes, int first, int end,

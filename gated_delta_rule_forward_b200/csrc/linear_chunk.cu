@@ -295,22 +295,19 @@ __device__ __forceinline__ void split_pair(uint32_t x, float w0, float w1, uint3
 // LONG: phase 2 chains any number of segments (kLinSelfChain otherwise) or from copied start states, whose code costs
 // the others registers.
 template <int DA, int DC, bool PHASE1, bool YF32, bool LONG>
-__global__ void __launch_bounds__(NTHREADS, 1)
-    linear_chunk_kernel(const __grid_constant__ LinProblem p, const __grid_constant__ LinChunkMaps maps,
-                        const LinRunSel sel) {
+__device__ __forceinline__ void chunk_run(const LinProblem &p, const LinChunkMaps &maps, const LinRun &r) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + (-smem_u32(smem_raw) & 1023u);   // an offset, so that accesses stay shared ones
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform in the compiler's eyes, and so the branches on it
-  const int ri = sel.run[blockIdx.x % sel.n];
-  const LinRun &r = p.run[ri];
+  const unsigned blocks = gridDim.x / p.nrun, block = blockIdx.x % blocks;   // of this run's
   if (warp == W_COPY && lane < 3) prefetch_tmap(&maps.m[lane == 0 ? r.ib : lane == 1 ? r.ic : r.ia]);
   const bool rev = r.reverse != 0;
   const bool zero_rest = !PHASE1 && !YF32 && p.zero_rest;
   int rest_first = 0, rest_end = p.T;
   if (zero_rest) rest_first = lin_cu(p, 0), rest_end = lin_cu(p, p.N);
-  const LinItem it = lin_item(p, blockIdx.x / sel.n);
-  if (zero_rest) lin_zero_rest(p, r.y, static_cast<size_t>(p.H) * DC * 2, rest_first, rest_end, blockIdx.x / sel.n, gridDim.x / sel.n);
+  const LinItem it = lin_item(p, block);
+  if (zero_rest) lin_zero_rest(p, r.y, static_cast<size_t>(p.H) * DC * 2, rest_first, rest_end, block, blocks);
   const int h = it.h;
   const bool last = rev ? it.g == 0 : it.g == it.nseg - 1;   // in the run's order
   if (!it.ok || (PHASE1 && last && (it.nseg == 1 || !r.s_final))) {
@@ -404,10 +401,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const bool three = PHASE1 || __shfl_sync(0xffffffffu, final_page != nullptr, 0);
   const int tail_i = rev ? 0 : nch - 1, tail_n = end - beg - C * (nch - 1);   // the only chunk that may be short
 
-  // The grid before: phase 1's states, or the chain kernel's.  (A sequence that runs whole
-  // needs nothing of it, and may run beside it.)
+  // The grid before: phase 1's states, or the chain kernel's.  Whoever reads them waits here itself.  (A sequence
+  // that runs whole reads only what the call was given, and may run beside it.)
   const float *start = r.X + static_cast<size_t>(it.slot) * DA * DC;
-  if (!sel.beside && (PHASE1 || it.nseg > 1)) griddep_wait();
+  if (PHASE1 || it.nseg > 1) griddep_wait();
   griddep_launch_dependents();
   if (PHASE1 && p.s0_copied && it.g == 0) {
     const float4 *src = reinterpret_cast<const float4 *>(r.s0 + (static_cast<size_t>(max(page, 0)) * p.H + h) * DA * DC);
@@ -436,7 +433,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int j = i > NST ? i - NST : PHASE1 && faulty ? 1 : 0; j < i; ++j)
         mbar_wait(reinterpret_cast<uint64_t *>(sm + M::LOAD) + j % NST, (j / NST) & 1);
     }
-    if (sel.beside) griddep_wait();   // what follows this grid follows the one beside it
+    // what follows this grid follows the one before it, whether or not any of its blocks had to wait
+    if (blockIdx.x == gridDim.x - 1) griddep_wait();
   } else if (warp > W_COPY) {
     // ---------------------------------------------------------------- MMAs
     // A warp for each kind, so that none waits behind another's operands; a product's
@@ -852,10 +850,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
 }
 
-template <int DA, int DC, bool PHASE1, bool YF32, bool LONG>
-cudaError_t launch(const LinProblem &p, const LinChunkMaps &maps, const LinRunSel &sel, bool pdl, cudaStream_t s) {
+// All runs of a phase in one launch, one run's blocks after another's.  A forward has one run, (DA, DC); a backward
+// dq's, dk's and dv's, the last (DA, DC), the others (DC, DA) and with y in fp32 if YF32, which a MIXED kernel has a
+// second body for.  (With the runs' blocks in turn, neighbouring SMs run different bodies: 8 sequences of 2048 tokens,
+// 8 heads, 128 x 64, 166 us for 100, and with one body 111 for 109.)
+template <int DA, int DC, bool PHASE1, bool MIXED, bool YF32, bool LONG>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    linear_chunk_kernel(const __grid_constant__ LinProblem p, const __grid_constant__ LinChunkMaps maps) {
+  const LinRun &r = lin_run(p);
+  if (MIXED && (r.dc != DC || r.y_f32)) chunk_run<DC, DA, PHASE1, YF32, LONG>(p, maps, r);
+  else chunk_run<DA, DC, PHASE1, false, LONG>(p, maps, r);
+}
+
+template <int DA, int DC, bool PHASE1, bool MIXED, bool YF32, bool LONG>
+cudaError_t launch(const LinProblem &p, const LinChunkMaps &maps, bool pdl, cudaStream_t s) {
   constexpr uint32_t SMEM = Smem<PHASE1>::BYTES;
-  auto kern = linear_chunk_kernel<DA, DC, PHASE1, YF32, LONG>;
+  auto kern = linear_chunk_kernel<DA, DC, PHASE1, MIXED, YF32, LONG>;
   // the kernel's limit on the current device, set by the first call there
   static std::atomic<unsigned long long> set{0};
   int dev = 0;
@@ -867,7 +877,7 @@ cudaError_t launch(const LinProblem &p, const LinChunkMaps &maps, const LinRunSe
     set.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(lin_blocks(p) * sel.n));
+  cfg.gridDim = dim3(static_cast<unsigned>(lin_blocks(p) * p.nrun));
   cfg.blockDim = dim3(NTHREADS);
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
@@ -876,16 +886,18 @@ cudaError_t launch(const LinProblem &p, const LinChunkMaps &maps, const LinRunSe
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, p, maps, sel);
+  return cudaLaunchKernelEx(&cfg, kern, p, maps);
 }
 
-template <bool PHASE1, bool YF32, bool LONG>
-cudaError_t launch_shape(int da, int dc, const LinProblem &p, const LinChunkMaps &m, const LinRunSel &sel, bool pdl,
-                         cudaStream_t s) {
-  if (da == 128 && dc == 128) return launch<128, 128, PHASE1, YF32, LONG>(p, m, sel, pdl, s);
-  if (da == 128 && dc == 64) return launch<128, 64, PHASE1, YF32, LONG>(p, m, sel, pdl, s);
-  if (da == 64 && dc == 128) return launch<64, 128, PHASE1, YF32, LONG>(p, m, sel, pdl, s);
-  return launch<64, 64, PHASE1, YF32, LONG>(p, m, sel, pdl, s);
+template <int DA, int DC>
+cudaError_t launch_kind(const LinProblem &p, const LinChunkMaps &m, bool phase1, bool pdl, cudaStream_t s) {
+  const bool backward = p.nrun == kLinMaxRuns;
+  if (backward && phase1 && DA != DC) return launch<DA, DC, true, DA != DC, false, false>(p, m, pdl, s);
+  if (phase1) return launch<DA, DC, true, false, false, false>(p, m, pdl, s);
+  if (backward && p.run[0].y_f32) return launch<DA, DC, false, true, true, false>(p, m, pdl, s);
+  if (backward && DA != DC) return launch<DA, DC, false, DA != DC, false, false>(p, m, pdl, s);
+  if (!p.chained && (p.G > kLinSelfChain || p.s0_copied)) return launch<DA, DC, false, false, false, true>(p, m, pdl, s);   // (a forward)
+  return launch<DA, DC, false, false, false, false>(p, m, pdl, s);
 }
 
 }  // namespace
@@ -923,30 +935,11 @@ bool gdr_linear_chunk_maps(const gdr::LinProblem &p, gdr::LinChunkMaps *maps) {
 
 cudaError_t gdr_launch_linear_chunk(const gdr::LinProblem &p, const gdr::LinChunkMaps &maps, bool phase1, bool pdl,
                                     cudaStream_t s) {
-  // one launch for all runs of a shape and output type, so that they read their common tensors at about the same time
-  bool done[gdr::kLinMaxRuns] = {};
-  for (int i = 0; i < p.nrun; ++i) {
-    if (done[i]) continue;
-    const gdr::LinRun &a = p.run[i];
-    gdr::LinRunSel sel = {};
-    for (int j = i; j < p.nrun; ++j) {
-      const gdr::LinRun &b = p.run[j];
-      if (done[j] || b.da != a.da || b.dc != a.dc || (!phase1 && b.y_f32 != a.y_f32)) continue;
-      sel.run[sel.n++] = j;
-      done[j] = true;
-    }
-    // the phase's first launch waits for the phase before; the others start once all of its CTAs are past that
-    // wait, run beside it and end after it
-    sel.beside = i > 0;
-    const bool dep = pdl || sel.beside;
-    const bool longer = !p.chained && (p.G > gdr::kLinSelfChain || p.s0_copied);   // (a forward: no y_f32)
-    const cudaError_t e = phase1    ? gdr::tc::launch_shape<true, false, false>(a.da, a.dc, p, maps, sel, dep, s)
-                          : a.y_f32 ? gdr::tc::launch_shape<false, true, false>(a.da, a.dc, p, maps, sel, dep, s)
-                          : longer  ? gdr::tc::launch_shape<false, false, true>(a.da, a.dc, p, maps, sel, dep, s)
-                                    : gdr::tc::launch_shape<false, false, false>(a.da, a.dc, p, maps, sel, dep, s);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  const gdr::LinRun &r = p.run[p.nrun - 1];   // o's or dv's: (dk, dv)
+  if (r.da == 128 && r.dc == 128) return gdr::tc::launch_kind<128, 128>(p, maps, phase1, pdl, s);
+  if (r.da == 128) return gdr::tc::launch_kind<128, 64>(p, maps, phase1, pdl, s);
+  if (r.dc == 128) return gdr::tc::launch_kind<64, 128>(p, maps, phase1, pdl, s);
+  return gdr::tc::launch_kind<64, 64>(p, maps, phase1, pdl, s);
 }
 
 int gdr_linear_read_device_error(cudaStream_t stream) {

@@ -10,12 +10,6 @@ namespace gdr {
 struct LinChunkMaps {
   CUtensorMap m[4];   // of LinProblem::t
 };
-// The runs of one launch (all of one shape).
-struct LinRunSel {
-  int n;
-  int run[kLinMaxRuns];
-  bool beside;   // a programmatic dependent of another launch of its phase, with which it shares only inputs
-};
 
 }  // namespace gdr
 

@@ -33,26 +33,26 @@ __device__ __forceinline__ void copy16(uint32_t dst, const float *src) {
 }
 
 template <int DA, int DC, bool PHASE1>
-__global__ void __launch_bounds__(DC * 8 / NC) linear_token_kernel(const __grid_constant__ LinProblem p, int ir,
-                                                              bool beside) {
+constexpr int smem_floats = 2 * TT * ((PHASE1 ? 1 : 2) * DA + DC);
+
+template <int DA, int DC, bool PHASE1>
+__device__ __forceinline__ void token_run(const LinProblem &p, const LinRun &r, float *smem) {
   constexpr int R = DA / 32, NT = DC * 8 / NC, HC = NC / 2;
-  __shared__ __align__(16) float ta[2][PHASE1 ? 1 : TT][DA], tb[2][TT][DA], tcol[2][TT][DC];
-  // In every thread, at the start or (a run beside the phase's first) at the end: a grid may not
-  // end before the one it depends on.
-  if (!beside) tc::griddep_wait();
+  float(*tb)[TT][DA] = reinterpret_cast<float(*)[TT][DA]>(smem);
+  float(*tcol)[TT][DC] = reinterpret_cast<float(*)[TT][DC]>(smem + 2 * TT * DA);
+  float(*ta)[TT][DA] = reinterpret_cast<float(*)[TT][DA]>(smem + 2 * TT * (DA + DC));   // (not in phase 1)
+  tc::griddep_wait();
   tc::griddep_launch_dependents();
-  const LinRun &r = p.run[ir];
   const int tid = threadIdx.x, lane = tid & 31;
+  const unsigned blocks = gridDim.x / p.nrun, block = blockIdx.x % blocks;   // of this run's
   if (!PHASE1 && p.zero_rest && !r.y_f32)
-    lin_zero_rest(p, r.y, static_cast<size_t>(p.H) * DC * 4, lin_cu(p, 0), lin_cu(p, p.N), blockIdx.x, gridDim.x);
-  const LinItem it = lin_item(p, blockIdx.x);
+    lin_zero_rest(p, r.y, static_cast<size_t>(p.H) * DC * 4, lin_cu(p, 0), lin_cu(p, p.N), block, blocks);
+  if (tid >= NT) return;   // a narrow run beside wide ones
+  const LinItem it = lin_item(p, block);
   const int h = it.h;
   const bool rev = r.reverse != 0;
   const bool last = rev ? it.g == 0 : it.g == it.nseg - 1;    // in the run's order
-  if (!it.ok || (PHASE1 && last && (it.nseg == 1 || !r.s_final))) {
-    if (beside) tc::griddep_wait();
-    return;
-  }
+  if (!it.ok || (PHASE1 && last && (it.nseg == 1 || !r.s_final))) return;
   const float ld = __ldg(p.log_decay + h);
   const int page = lin_page(p, it.n);
 
@@ -225,42 +225,50 @@ __global__ void __launch_bounds__(DC * 8 / NC) linear_token_kernel(const __grid_
         }
       }
   }
-  if (beside) tc::griddep_wait();
 }
 
-template <int DA, int DC, bool PHASE1>
-cudaError_t launch_run(const LinProblem &p, int ir, bool pdl, cudaStream_t s) {
+// All runs of a phase in one launch, one run's blocks after another's.  A forward has one run, (DA, DC); a backward
+// dq's, dk's and dv's, the last (DA, DC) and, if MIXED, the others (DC, DA).
+template <int DA, int DC, bool MIXED>
+constexpr int kBlock = (MIXED && DA > DC ? DA : DC) * 8 / NC;
+
+template <int DA, int DC, bool PHASE1, bool MIXED>
+__global__ void __launch_bounds__(kBlock<DA, DC, MIXED>) linear_token_kernel(const __grid_constant__ LinProblem p) {
+  constexpr int own = smem_floats<DA, DC, PHASE1>, other = MIXED ? smem_floats<DC, DA, PHASE1> : 0;
+  __shared__ __align__(16) float smem[own > other ? own : other];
+  const LinRun &r = lin_run(p);
+  if (MIXED && r.dc != DC) token_run<DC, DA, PHASE1>(p, r, smem);
+  else token_run<DA, DC, PHASE1>(p, r, smem);
+}
+
+template <int DA, int DC, bool PHASE1, bool MIXED>
+cudaError_t launch(const LinProblem &p, bool pdl, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(lin_blocks(p)));
-  cfg.blockDim = dim3(DC * 8 / NC);
+  cfg.gridDim = dim3(static_cast<unsigned>(lin_blocks(p) * p.nrun));
+  cfg.blockDim = dim3(kBlock<DA, DC, MIXED>);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, linear_token_kernel<DA, DC, PHASE1>, p, ir, ir > 0);
+  return cudaLaunchKernelEx(&cfg, linear_token_kernel<DA, DC, PHASE1, MIXED>, p);
 }
 
-template <bool PHASE1>
-cudaError_t launch_shape(const LinProblem &p, int ir, bool pdl, cudaStream_t s) {
-  const LinRun &r = p.run[ir];
-  if (r.da == 128 && r.dc == 128) return launch_run<128, 128, PHASE1>(p, ir, pdl, s);
-  if (r.da == 128) return launch_run<128, 64, PHASE1>(p, ir, pdl, s);
-  if (r.dc == 128) return launch_run<64, 128, PHASE1>(p, ir, pdl, s);
-  return launch_run<64, 64, PHASE1>(p, ir, pdl, s);
+template <int DA, int DC>
+cudaError_t launch_kind(const LinProblem &p, bool phase1, bool pdl, cudaStream_t s) {
+  if (DA != DC && p.nrun == kLinMaxRuns)
+    return phase1 ? launch<DA, DC, true, DA != DC>(p, pdl, s) : launch<DA, DC, false, DA != DC>(p, pdl, s);
+  return phase1 ? launch<DA, DC, true, false>(p, pdl, s) : launch<DA, DC, false, false>(p, pdl, s);
 }
 
 }  // namespace
 }  // namespace gdr
 
 cudaError_t gdr_launch_linear_token(const gdr::LinProblem &p, bool phase1, bool pdl, cudaStream_t s) {
-  for (int i = 0; i < p.nrun; ++i) {
-    // the first run waits for the phase before; the others start once all of its CTAs are past that wait, run
-    // beside it and end after it
-    const bool dep = pdl || i > 0;
-    const cudaError_t e = phase1 ? gdr::launch_shape<true>(p, i, dep, s) : gdr::launch_shape<false>(p, i, dep, s);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  const gdr::LinRun &r = p.run[p.nrun - 1];   // o's or dv's: (dk, dv)
+  if (r.da == 128 && r.dc == 128) return gdr::launch_kind<128, 128>(p, phase1, pdl, s);
+  if (r.da == 128) return gdr::launch_kind<128, 64>(p, phase1, pdl, s);
+  if (r.dc == 128) return gdr::launch_kind<64, 128>(p, phase1, pdl, s);
+  return gdr::launch_kind<64, 64>(p, phase1, pdl, s);
 }

@@ -721,3 +721,29 @@ def test_empty_sequences_of_narrow_values(dtype):
     fine()
     assert all(torch.equal(a, b) for d in dense for a, b in zip(d, dense[0]))
     ref.check_forward(q[0], k[0], v[0], ld, None, 1.0, dense[-1][0][0], dense[-1][1][0])
+
+
+@pytest.mark.parametrize("dtype,Hk,H,dk,dv,lens", [(BF16, 2, 2, 128, 64, [1500]), (BF16, 1, 3, 64, 128, [900, 0, 1, 411]),
+                                                   (BF16, 1, 2, 128, 128, [1100]), (BF16, 1, 2, 64, 64, [40, 1000, 3]),
+                                                   (F32, 1, 2, 64, 128, [700]), (F32, 2, 2, 128, 64, [30, 600, 0, 5])])
+def test_backward_in_segments_again_and_again(dtype, Hk, H, dk, dv, lens):
+    """Runs of different shapes and output types in one call, every call's segment states in memory that held NaN
+    before: the same bits each time."""
+    T, N = sum(lens), len(lens)
+    q, k, v, g = tensors(81, 1, T, Hk, H, dk, dv, dtype)
+    do, S0, dS = randn(g, 1, T, H, dv, dtype=dtype), randn(g, N, H, dk, dv), randn(g, N, H, dk, dv)
+    ld = decays(H)
+    cu = torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32) if N > 1 else None
+    want = None
+    for _ in range(20):
+        held = [torch.full((n,), float("nan"), device="cuda") for n in (1 << 18, 1 << 20, 1 << 22, 1 << 22)]
+        del held
+        x = gdr.linear_backward(q, k, v, do, log_decay=ld, initial_state=S0, d_final_state=dS, cu_seqlens=cu, scale=0.3)
+        want = want or x
+        assert all(torch.equal(x[n], want[n]) for n in x)
+    fine()
+    t = 0
+    for n, L in enumerate(lens):
+        s, t = slice(t, t + L), t + L
+        ref.check_grads(q[0, s], k[0, s], v[0, s], do[0, s], ld, S0[n], dS[n], 0.3,
+                        (want["q"][0, s], want["k"][0, s], want["v"][0, s], want["initial_state"][n]), f"sequence {n}")
