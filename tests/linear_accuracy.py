@@ -11,14 +11,14 @@ token (fp32).
 States, as a relative RMS per head.  An update of the state rounds once, by at
 most 2^-24 of it, and updates further back than the state's memory are
 forgotten, so that M = min(updates, 1 / (2 (1 - decay))) of them, independent,
-give at most sqrt(M) 2^-24 (their RMS is 0.4 of that).  A block's sum goes
+give sqrt(M) 0.41 2^-24 (2^-24 / sqrt(3), times 0.72 for values spread over a binade); half of 2^-24 is taken.  A block's sum goes
 through 12 accumulations of the tensor cores (four steps of 16 tokens, three terms of the
 weighted values), which may drop up to 2^-23 of the sum each: half of it on average,
 12 2^-24 = 0.75 2^-20 altogether.  So
-    limit = 2^-20 + sqrt(M) 2^-24            (bf16, an update a block)
+    limit = 2^-20 + 0.5 sqrt(M) 2^-24        (bf16, an update a block)
     limit = 2 (2 + sqrt(M)) 2^-24            (fp32 and decode, an update a token; three roundings each)
 Two bf16 terms in place of three lose 2.6e-6 of each weighted value; one fp32 value of
-lambda (or of lambda^64) up to 2^-25 an update, all the same way.
+lambda (of lambda^64, or of the power that a segment's state is chained with) up to 2^-25 an update, all the same way.
 
 Outputs (bf16), element by element.  P with its decays and the state operand are
 rounded to bf16 (2^-8 of each value, on disjoint parts of the sum), everything else in
@@ -42,7 +42,7 @@ def fp32(log_decay):
 def state_limit(updates, decay, dtype):
     memory = min(float(updates), 0.5 / (1.0 - decay)) if decay < 1.0 else float(updates)
     if dtype == torch.bfloat16:
-        return 2.0 ** -20 + math.sqrt(memory) * 2.0 ** -24
+        return 2.0 ** -20 + 0.5 * math.sqrt(memory) * 2.0 ** -24
     return 2.0 * (2.0 + math.sqrt(memory)) * 2.0 ** -24
 
 
@@ -141,6 +141,20 @@ def emulated_run(a, b, c, log_decay, S0=None, reverse=False, bscale=1.0, yscale=
             dS, rest = dS + z.T @ term, rest - term
         S = (decay.next() if n == C else pw[n]) * S + dS
     return y.to(torch.bfloat16), S
+
+
+def emulated_chain(b, c, log_decay, seg, parts=2):
+    """The state after T tokens as the chain of its segments' states, which are right, with the power of lambda that
+    joins them in `parts` fp32 values."""
+    x = math.exp(fp32(log_decay) * seg)
+    hi = torch.tensor(x, dtype=torch.float64).float()
+    lo = torch.tensor((x - hi.double().item()) if parts == 2 else 0.0).float()
+    fma = lambda f, s, y: (f.double() * s.double() + y.double()).float()
+    S = torch.zeros(b.shape[1], c.shape[1])
+    for t in range(0, b.shape[0], seg):
+        X = decode_states(b[t:t + seg], c[t:t + seg], log_decay, torch.zeros_like(S)).float()
+        S = fma(hi, S, fma(lo, S, X))
+    return S
 
 
 def decode_states(k, v, log_decay, S0):

@@ -54,6 +54,16 @@ def test_states_need_both_decays():
         acc.check_state(acc.emulated_run(a, b, c, ld, S0, fixed=True)[1], S, T, ld, BF16, "one")
 
 
+def test_chains_need_the_power_in_two_parts():
+    seg, G = 448, 147
+    ld = acc.worst_decay(-5e-6, seg)
+    _, b, c, _ = tensors(6, seg * G, 8, 16, positive=True)
+    S = acc.decode_states(b, c, ld, torch.zeros(8, 16))
+    acc.check_state(acc.emulated_chain(b, c, ld, seg), S, seg * G, ld, BF16, "two parts")
+    with pytest.raises(AssertionError, match="relative RMS"):
+        acc.check_state(acc.emulated_chain(b, c, ld, seg, parts=1), S, seg * G, ld, BF16, "one part")
+
+
 @pytest.mark.parametrize("reverse", [False, True])
 def test_outputs_need_the_right_state(reverse):
     T, ld = 333, -0.01
