@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kChainThreads) linear_chain_kernel(const LinPr
     if (nseg == 1) continue;
     const int tail = len - (nseg - 1) * p.seg;   // tokens of the last segment
     const float ld = __ldg(p.log_decay + h);
-    const float full = lin_pow64(ld, p.seg), ftail = tail == p.seg ? full : lin_pow64(ld, tail);
+    const float2 full = lin_pow64_parts(ld, p.seg), ftail = tail == p.seg ? full : lin_pow64_parts(ld, tail);
     const int page = lin_page(p, n);
     float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r.s0 && page >= 0) {
@@ -64,11 +64,11 @@ __global__ void __launch_bounds__(kChainThreads) linear_chain_kernel(const LinPr
         if (i >= nseg) break;
         X[(r.reverse ? nseg - 1 - i : i) * xs] = cur;
         if (i == nseg - 1 && !fin) break;
-        const float f = i == (r.reverse ? 0 : nseg - 1) ? ftail : full;   // the sequence's last segment may be short
-        cur.x = fmaf(f, cur.x, d[k].x);
-        cur.y = fmaf(f, cur.y, d[k].y);
-        cur.z = fmaf(f, cur.z, d[k].z);
-        cur.w = fmaf(f, cur.w, d[k].w);
+        const float2 f = i == (r.reverse ? 0 : nseg - 1) ? ftail : full;   // the sequence's last segment may be short
+        cur.x = fmaf(f.x, cur.x, fmaf(f.y, cur.x, d[k].x));
+        cur.y = fmaf(f.x, cur.y, fmaf(f.y, cur.y, d[k].y));
+        cur.z = fmaf(f.x, cur.z, fmaf(f.y, cur.z, d[k].z));
+        cur.w = fmaf(f.x, cur.w, fmaf(f.y, cur.w, d[k].w));
       }
     }
     if (fin) *fin = cur;

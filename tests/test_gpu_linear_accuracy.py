@@ -95,7 +95,7 @@ def test_states_are_kept_in_32_bits(dtype, N, T, dk, dv):
             acc.check_state(x["initial_state"][n, h], want, T, ld[h], dtype, f"row {n} head {h} d_initial_state")
 
 
-@pytest.mark.parametrize("dtype,T,H,heads", [(BF16, 16384, 150, (0, 77, 149)), (BF16, 16384, 2, (0, 1)),
+@pytest.mark.parametrize("dtype,T,H,heads", [(BF16, 16384, 150, (0, 77, 149)), (BF16, 65536, 1, (0,)), (BF16, 16384, 2, (0, 1)),
                                              (F32, 8192, 300, (0, 299)), (F32, 16384, 1, (0,))])
 def test_states_of_long_memory(dtype, T, H, heads):
     """Values of one sign and decays whose power over a chunk, a token or a segment lies half way between two fp32
