@@ -25,11 +25,14 @@ gdr_status_t fail(gdr_status_t st, const std::string &why) {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-bool injected_fault(const char *kind) {
+// What GDR_FAULT asks for (host-side fault injection).
+enum class Fault { None, Launch, Wait };
+Fault injected_fault() {
   const char *f = std::getenv("GDR_FAULT");
-  return f && std::strcmp(f, kind) == 0;
+  if (!f) return Fault::None;
+  return std::strcmp(f, "launch") == 0 ? Fault::Launch : std::strcmp(f, "wait") == 0 ? Fault::Wait : Fault::None;
 }
-bool injected_launch_fault() { return injected_fault("launch"); }
+bool injected_launch_fault() { return injected_fault() == Fault::Launch; }
 
 gdr_status_t check_cuda(cudaError_t e, const char *what) {
   if (e == cudaSuccess) return GDR_OK;
@@ -524,10 +527,11 @@ gdr_status_t gdr_linear_forward(int dtype, int B, int T, int Hk, int H, int dk, 
     return fail(GDR_ERR_INVALID_ARG, "the workspace must be at least gdr_linear_workspace_size() bytes");
   if (need && !aligned16(workspace)) return fail(GDR_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
   if (T == 0 && !a->final_state) return GDR_OK;
-  if (injected_launch_fault()) return fail(GDR_ERR_CUDA, "injected launch failure (GDR_FAULT=launch)");
+  const Fault fault = injected_fault();   // one look at the environment a call
+  if (fault == Fault::Launch) return fail(GDR_ERR_CUDA, "injected launch failure (GDR_FAULT=launch)");
   p.cu = a->cu_seqlens; p.slots = a->state_slots; p.pages = a->state_slots ? a->pages : N;
   p.zero_rest = a->cu_seqlens && a->zero_rest;
-  p.fault = injected_fault("wait");
+  p.fault = fault == Fault::Wait;
   p.log_decay = a->log_decay;
   gdr::LinRun &r = p.run[0];
   r.yscale = scale; r.y = a->o; r.s0 = a->initial_state; r.s_final = a->final_state;
@@ -569,10 +573,11 @@ gdr_status_t gdr_linear_backward(int dtype, int B, int T, int Hk, int H, int dk,
     return fail(GDR_ERR_INVALID_ARG, "the workspace must be at least gdr_linear_workspace_size() bytes");
   if (need && !aligned16(workspace)) return fail(GDR_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
   if (T == 0 && !g->d_initial_state) return GDR_OK;
-  if (injected_launch_fault()) return fail(GDR_ERR_CUDA, "injected launch failure (GDR_FAULT=launch)");
+  const Fault fault = injected_fault();   // one look at the environment a call
+  if (fault == Fault::Launch) return fail(GDR_ERR_CUDA, "injected launch failure (GDR_FAULT=launch)");
   p.cu = a->cu_seqlens; p.pages = N;
   p.zero_rest = a->cu_seqlens && a->zero_rest;
-  p.fault = injected_fault("wait");
+  p.fault = fault == Fault::Wait;
   p.log_decay = a->log_decay;
   float *dq32 = nullptr, *dk32 = nullptr;
   if (H != Hk && T > 0) {
