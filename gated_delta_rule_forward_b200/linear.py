@@ -75,7 +75,7 @@ def _strided(t, name, shape, dtype, device):
 
 
 def _shape(q, k, v, log_decay, cu_seqlens):
-    if q.dim() != 4 or v.dim() != 4:
+    if q is None or v is None or q.dim() != 4 or v.dim() != 4:
         raise ValueError("q must be [B,T,Hk,dk] and v [B,T,H,dv]")
     B, T, Hk, dk = q.shape
     H, dv = v.shape[2], v.shape[3]
@@ -87,12 +87,14 @@ def _shape(q, k, v, log_decay, cu_seqlens):
         raise ValueError("q, k, v must be bf16 or fp32")
     if H and (Hk == 0 or H % Hk):
         raise ValueError(f"v's {H} heads must be a multiple of the {Hk} heads of q and k")
-    a = LinearArgs(q=q.data_ptr(), k=k.data_ptr(), v=v.data_ptr(), log_decay=log_decay.data_ptr())
-    for t, name, shape in ((q, "q", q.shape), (k, "k", q.shape), (v, "v", (B, T, H, dv))):
-        stride = _strided(t, name, shape, dtype, dev)
-        if stride is not None:
-            setattr(a, name + "_stride", stride)
+    strides = (_strided(q, "q", q.shape, dtype, dev), _strided(k, "k", q.shape, dtype, dev),
+               _strided(v, "v", (B, T, H, dv), dtype, dev))
     _dense(log_decay, "log_decay", (H,), torch.float32, dev)
+    a = LinearArgs(q=q.data_ptr(), k=k.data_ptr(), v=v.data_ptr(), log_decay=log_decay.data_ptr())
+    if strides != (None, None, None):
+        for name, stride in zip(("q_stride", "k_stride", "v_stride"), strides):
+            if stride is not None:
+                setattr(a, name, stride)
     N = B
     if cu_seqlens is not None:
         if B != 1:
@@ -171,8 +173,8 @@ def linear_backward(q, k, v, d_o, *, log_decay, initial_state=None, d_final_stat
     a, dims = _shape(q, k, v, log_decay, cu_seqlens)
     dt, B, T, Hk, H, dk, dv, N = dims
     dev, f32 = q.device, torch.float32
-    g = LinearGrads(d_o=d_o.data_ptr())
     stride = _strided(d_o, "d_o", v.shape, q.dtype, dev)
+    g = LinearGrads(d_o=d_o.data_ptr())
     if stride is not None:
         g.d_o_stride = stride
     if initial_state is not None:
@@ -202,7 +204,7 @@ def linear_decode_step(q, k, v, state, *, log_decay, state_slots=None, scale=1.0
     state_slots[n] (int32 [N], device; None: page n).  A row whose slot lies
     outside the pool is padding: its o is zeros and it touches no state.  The
     slots inside the pool must differ from one another.  Returns o [N,H,dv]."""
-    if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
+    if q is None or v is None or state is None or q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
         raise ValueError("q must be [N,Hk,dk], v [N,H,dv] and state [pages,H,dk,dv]")
     N, Hk, dk = q.shape
     H, dv = v.shape[1:]
@@ -241,7 +243,7 @@ def copy_states(pool, src, dst, *, stream=None):
     (fp32, contiguous, CUDA; states of any variant): for each i in turn, page
     dst[i] of every layer becomes a copy of page src[i], or zeros where src[i] is
     -1.  src and dst are host sequences of ints."""
-    if pool.dim() not in (4, 5):
+    if pool is None or pool.dim() not in (4, 5):
         raise ValueError("pool must be [pages,H,dk,dv] or [layers,pages,H,dk,dv]")
     if pool.device.type != "cuda":
         raise ValueError("pool must be a CUDA tensor (there is no CPU path)")

@@ -241,3 +241,39 @@ def test_state_cache_keeps_its_pages_when_a_copy_fails(monkeypatch):
         with pytest.raises(_lib.GdrError):
             call()
         assert c.live_pages == [a[1]] and c.free_pages == 2
+
+
+def _fake_calls():
+    """Keyword calls of the binding on stand-ins for CUDA tensors (no storage behind them)."""
+    bf = dict(device="cuda", dtype=torch.bfloat16)
+    q, k, v, d_o = (torch.empty(2, 5, 4, 64, **bf) for _ in range(4))
+    ld = torch.empty(4, device="cuda")
+    row = {n: torch.empty(2, 4, 64, **bf) for n in "qkv"}
+    return [(gdr.linear_forward, dict(q=q, k=k, v=v, log_decay=ld)),
+            (gdr.linear_backward, dict(q=q, k=k, v=v, d_o=d_o, log_decay=ld)),
+            (gdr.linear_decode_step, dict(row, state=torch.empty(2, 4, 64, 64, device="cuda"), log_decay=ld))]
+
+
+@pytest.mark.parametrize("which", range(3))
+def test_binding_says_what_is_missing(which):
+    """None, and tensors of another device, type or shape, are refused as arguments, before anything reads them."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode():
+        call, good = _fake_calls()[which]
+        for name in good:
+            with pytest.raises(ValueError, match=rf"\b{name}\b"):
+                call(**dict(good, **{name: None}))
+            if name == "q":                       # the others are compared with it
+                continue
+            with pytest.raises(ValueError, match=rf"\b{name}\b must be"):
+                call(**dict(good, **{name: torch.empty(good[name].shape, dtype=good[name].dtype)}))
+            with pytest.raises(ValueError, match=rf"\b{name}\b must be"):
+                call(**dict(good, **{name: good[name].to(torch.float16)}))
+            if name in ("k", "d_o", "log_decay"):
+                with pytest.raises(ValueError, match=rf"\b{name}\b must have shape"):
+                    call(**dict(good, **{name: good[name][:1]}))
+
+
+def test_copies_need_a_pool():
+    with pytest.raises(ValueError, match="pool must be"):
+        gdr.copy_states(None, [0], [1])
