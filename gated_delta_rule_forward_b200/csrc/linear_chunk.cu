@@ -15,9 +15,8 @@
 //     O2^T [dc][t]  = c^T P^T        M128 N64  K = 64   (P back through shared memory in bf16)
 // and Y^T = yscale (Gamma_t O1^T + O2^T).  The fp32 state lives in registers of
 // 8 warps: lane dc of a quad, half of da per thread; S <- lambda^n S + dS
-// is one pass over it.  What bounds the sweep on the chip is the 128 bytes a clock
-// of shared memory: weighting c on its way into tensor memory, rather than b in
-// place, takes 64 KB of a chunk's 272 KB off it.
+// is one pass over it.  c is weighted on its way into tensor memory, rather than b in
+// place, which takes 64 KB of a chunk's 272 KB off shared memory.
 //
 // Rounding.  The products' inputs are exact bf16 except three: w c, P and the
 // S^T operand.  w c enters the state, which is fp32, so it is split into three
@@ -40,8 +39,11 @@
 // 1.30 GHz; 8 sequences of 2048 tokens, 8 heads, 59 us forward (1.73 GHz) and 112 us backward.
 // With 192 runs of 32 chunks the tensor pipe is active 42% of the time and 53% of the issue
 // slots are taken (1.73 GHz); a chunk takes about 2500 cycles, and value widths of 64 hardly
-// less (144 runs of 32 chunks: 67 us for 72).  Products: 64 KB of P's operands and so on
-// would take 1300.  Dropped after measurement: O1 and O2 in one accumulator (64k 385 us, backward
+// less (144 runs of 32 chunks: 67 us for 72).  So neither the tensor pipe nor DRAM (43% at most)
+// bounds it, nor shared memory, whose 208 KB a chunk (48 copied in, 32 read for P, 16 a term of dS, 16 for O1, 24 for O2,
+// 16 of c weighted, 8 of P and 32 of output rows through it) are 1625 cycles at 128 bytes a clock: the
+// hand-overs from one kind of warp to the next do, and the issue slots of the slowest kind.
+// Dropped after measurement: O1 and O2 in one accumulator (64k 385 us, backward
 // 118), one issuing warp for all products (404), weighting with packed bf16 arithmetic (no change).
 #include <atomic>
 #include <type_traits>
@@ -62,8 +64,7 @@ constexpr int C = 64;
 // warps 0-7 state, 8-15 output, 16-23 prep, then one for the copies and one for each of
 // the three kinds of products
 constexpr int NSTATE = 8, NOUT = 8, NPREP = 8;
-constexpr int W_OUT = NSTATE, W_PREP = W_OUT + NOUT, W_COPY = W_PREP + NPREP, W_MMA_P = W_COPY + 1, W_MMA_DS = W_COPY + 2,
-              W_MMA_O = W_COPY + 3;
+constexpr int W_OUT = NSTATE, W_PREP = W_OUT + NOUT, W_COPY = W_PREP + NPREP, W_MMA_P = W_COPY + 1, W_MMA_DS = W_COPY + 2;   // the last one: O
 constexpr int NTHREADS = 32 * (W_COPY + 4);
 // registers a thread: 72 at launch, moved to the threads that hold the state
 constexpr int R_STATE = 112, R_OUT = 64, R_PREP = 56, R_CTL = 40;
