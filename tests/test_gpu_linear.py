@@ -747,3 +747,44 @@ def test_backward_in_segments_again_and_again(dtype, Hk, H, dk, dv, lens):
         s, t = slice(t, t + L), t + L
         ref.check_grads(q[0, s], k[0, s], v[0, s], do[0, s], ld, S0[n], dS[n], 0.3,
                         (want["q"][0, s], want["k"][0, s], want["v"][0, s], want["initial_state"][n]), f"sequence {n}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_packed_captured(dtype):
+    """A replayed prefill into a pool and a replayed packed backward take the offsets, slots, decays and tokens that
+    their buffers hold at the replay: other lengths, empty sequences and rows of no sequence among them."""
+    T, N, Hk, H, dk, dv, pages = 1600, 3, 1, 2, 128, 64, 5
+    g = gen(91)
+    q, k = (randn(g, 1, T, Hk, dk, dtype=dtype) for _ in range(2))
+    v, do = (randn(g, 1, T, H, dv, dtype=dtype) for _ in range(2))
+    ld = torch.empty(H, device="cuda")
+    cu, slots = torch.empty(N + 1, device="cuda", dtype=torch.int32), torch.empty(N, device="cuda", dtype=torch.int32)
+    start, S0 = randn(g, pages, H, dk, dv), randn(g, N, H, dk, dv)
+    pool = start.clone()
+
+    def call(pool):
+        o, _ = gdr.linear_forward(q, k, v, log_decay=ld, initial_state=pool, final_state=pool, cu_seqlens=cu,
+                                  state_slots=slots, scale=0.1)
+        x = gdr.linear_backward(q, k, v, do, log_decay=ld, initial_state=S0, cu_seqlens=cu, scale=0.1)
+        return [o, *x.values()]
+
+    def fill(lens, rows, decay):
+        cu.copy_(torch.tensor([0] + lens).cumsum(0))
+        slots.copy_(torch.tensor(rows))
+        ld.copy_(torch.tensor(decay))
+        pool.copy_(start)
+
+    fill([1600, 0, 0], [0, 1, 2], [-0.1, -0.1])
+    call(pool)                                            # before the capture
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call(pool)
+    for lens, rows, decay in (([3, 1500, 7], [2, 0, 4], [-0.01, 0.0]), ([0, 0, 0], [1, 2, 3], [-0.3, -2.0]),
+                              ([700, 0, 800], [4, -1, 9], [-1e-3, float("-inf")])):
+        fill(lens, rows, decay)
+        graph.replay()
+        mine = start.clone()
+        want = call(mine)
+        fine()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(pool, mine), lens
+        assert all((x[:, sum(lens):] == 0).all() for x in got[:4])
