@@ -145,11 +145,17 @@ __device__ __forceinline__ LinItem lin_item(const LinProblem &p, int block) {
   return it;
 }
 
-// The run a block of a phase's launch belongs to (one run's blocks come after another's).  As comparisons: with the
-// index as a quotient the bf16 backward of 4 sequences of 4096 tokens, 16 heads, takes 218 us for 208.
-__device__ __forceinline__ const LinRun &lin_run(const LinProblem &p) {
+// The run a block of a phase's launch belongs to, and its block in that run: the runs' blocks in turn where one
+// body does all runs, which then read their common tensors together, one run's after another's where a run has a
+// body of its own, which neighbouring SMs then share.  (bf16 backward of 8 sequences of 2048 tokens, 8 heads, for seconds: 112
+// us in turn, 116 one after another; of 128 x 64, after a rest, 166 and 100.  The run's index as comparisons: as a quotient,
+// 4 sequences of 4096, 16 heads, take 218 us for 208.)
+template <bool IN_TURN>
+__device__ __forceinline__ const LinRun &lin_run(const LinProblem &p, unsigned &block) {
   const unsigned blocks = gridDim.x / p.nrun;
-  return p.run[blockIdx.x < blocks ? 0 : blockIdx.x < 2 * blocks ? 1 : 2];
+  const unsigned i = IN_TURN ? blockIdx.x % p.nrun : (blockIdx.x >= blocks) + (blockIdx.x >= 2 * blocks);
+  block = IN_TURN ? blockIdx.x / p.nrun : blockIdx.x - i * blocks;
+  return p.run[i == 0 ? 0 : i == 1 ? 1 : 2];
 }
 
 // This block's share of the zeros in a run's output rows of no sequence: [0, first) and [end, T), the offsets

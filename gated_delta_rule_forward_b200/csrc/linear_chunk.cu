@@ -34,12 +34,12 @@
 //     output (8 warps)   P of chunk i + 1 to bf16, the rows of chunk i
 // Only S -> operand -> O1 is a chain from chunk to chunk.
 //
-// Measured on a B200 (bf16, d = 128): 65536 tokens of 16 heads, both phases, 307 us in ten
-// calls after a rest and 364 us after seconds of them, when the power limit holds the clock at
-// 1.30 GHz; 8 sequences of 2048 tokens, 8 heads, 59 us forward (1.73 GHz) and 112 us backward.
-// With 192 runs of 32 chunks the tensor pipe is active 42% of the time and 53% of the issue
+// Measured on a B200 (bf16, d = 128): 65536 tokens of 16 heads, both phases, 306 us in thirty
+// calls after a rest and 363 us after seconds of them, when the power limit holds the clock at
+// 1.30 GHz; 8 sequences of 2048 tokens, 8 heads, 59 us forward and 112 us backward (1.73 GHz; 53 and 108 after a rest).
+// With 192 runs of 32 chunks the tensor pipe is active 43% of the time and 54% of the issue
 // slots are taken (1.73 GHz); a chunk takes about 2500 cycles, and value widths of 64 hardly
-// less (144 runs of 32 chunks: 67 us for 72).  So neither the tensor pipe nor DRAM (43% at most)
+// less (144 runs of 32 chunks: 67 us for 72).  So neither the tensor pipe nor DRAM (42% at most)
 // bounds it, nor shared memory, whose 208 KB a chunk (48 copied in, 32 read for P, 16 a term of dS, 16 for O1, 24 for O2,
 // 16 of c weighted, 8 of P and 32 of output rows through it) are 1625 cycles at 128 bytes a clock: the
 // hand-overs from one kind of warp to the next do, and the issue slots of the slowest kind.
@@ -296,19 +296,18 @@ __device__ __forceinline__ void split_pair(uint32_t x, float w0, float w1, uint3
 // LONG: phase 2 chains any number of segments (kLinSelfChain otherwise) or from copied start states, whose code costs
 // the others registers.
 template <int DA, int DC, bool PHASE1, bool YF32, bool LONG>
-__device__ __forceinline__ void chunk_run(const LinProblem &p, const LinChunkMaps &maps, const LinRun &r) {
+__device__ __forceinline__ void chunk_run(const LinProblem &p, const LinChunkMaps &maps, const LinRun &r, unsigned block) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + (-smem_u32(smem_raw) & 1023u);   // an offset, so that accesses stay shared ones
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform in the compiler's eyes, and so the branches on it
-  const unsigned blocks = gridDim.x / p.nrun, block = blockIdx.x % blocks;   // of this run's
   if (warp == W_COPY && lane < 3) prefetch_tmap(&maps.m[lane == 0 ? r.ib : lane == 1 ? r.ic : r.ia]);
   const bool rev = r.reverse != 0;
   const bool zero_rest = !PHASE1 && !YF32 && p.zero_rest;
   int rest_first = 0, rest_end = p.T;
   if (zero_rest) rest_first = lin_cu(p, 0), rest_end = lin_cu(p, p.N);
   const LinItem it = lin_item(p, block);
-  if (zero_rest) lin_zero_rest(p, r.y, static_cast<size_t>(p.H) * DC * 2, rest_first, rest_end, block, blocks);
+  if (zero_rest) lin_zero_rest(p, r.y, static_cast<size_t>(p.H) * DC * 2, rest_first, rest_end, block, gridDim.x / p.nrun);
   const int h = it.h;
   const bool last = rev ? it.g == 0 : it.g == it.nseg - 1;   // in the run's order
   if (!it.ok || (PHASE1 && last && (it.nseg == 1 || !r.s_final))) {
@@ -403,7 +402,7 @@ __device__ __forceinline__ void chunk_run(const LinProblem &p, const LinChunkMap
   const int tail_i = rev ? 0 : nch - 1, tail_n = end - beg - C * (nch - 1);   // the only chunk that may be short
 
   // The grid before: phase 1's states, or the chain kernel's.  Whoever reads them waits here itself.  (A sequence
-  // that runs whole reads only what the call was given, and may run beside it.)
+  // that runs whole reads only what the call was given, complete before phase 1 began, and may run beside it.)
   const float *start = r.X + static_cast<size_t>(it.slot) * DA * DC;
   if (PHASE1 || it.nseg > 1) griddep_wait();
   griddep_launch_dependents();
@@ -851,16 +850,15 @@ __device__ __forceinline__ void chunk_run(const LinProblem &p, const LinChunkMap
   }
 }
 
-// All runs of a phase in one launch, one run's blocks after another's.  A forward has one run, (DA, DC); a backward
-// dq's, dk's and dv's, the last (DA, DC), the others (DC, DA) and with y in fp32 if YF32, which a MIXED kernel has a
-// second body for.  (With the runs' blocks in turn, neighbouring SMs run different bodies: 8 sequences of 2048 tokens,
-// 8 heads, 128 x 64, 166 us for 100, and with one body 111 for 109.)
+// All runs of a phase in one launch.  A forward has one run, (DA, DC); a backward dq's, dk's and dv's, the last (DA, DC),
+// the others (DC, DA) and with y in fp32 if YF32, which a MIXED kernel has a second body for.
 template <int DA, int DC, bool PHASE1, bool MIXED, bool YF32, bool LONG>
 __global__ void __launch_bounds__(NTHREADS, 1)
     linear_chunk_kernel(const __grid_constant__ LinProblem p, const __grid_constant__ LinChunkMaps maps) {
-  const LinRun &r = lin_run(p);
-  if (MIXED && (r.dc != DC || r.y_f32)) chunk_run<DC, DA, PHASE1, YF32, LONG>(p, maps, r);
-  else chunk_run<DA, DC, PHASE1, false, LONG>(p, maps, r);
+  unsigned block;
+  const LinRun &r = lin_run<!MIXED>(p, block);
+  if (MIXED && (r.dc != DC || r.y_f32)) chunk_run<DC, DA, PHASE1, YF32, LONG>(p, maps, r, block);
+  else chunk_run<DA, DC, PHASE1, false, LONG>(p, maps, r, block);
 }
 
 template <int DA, int DC, bool PHASE1, bool MIXED, bool YF32, bool LONG>

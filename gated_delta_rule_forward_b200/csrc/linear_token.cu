@@ -12,7 +12,7 @@
 //
 // Bound by the FMA pipe: 3 d^2 multiplications and additions a token are 200 ns of an
 // SM at d = 128; it takes 380 (the pipe 57% active).  Two sequences of 500 tokens, 4
-// heads: 33 us in a graph; 74 of 300, 8 heads: 460 us.  With a column's rows over all 32
+// heads: 33 us in a graph; 74 of 300, 8 heads: 460 us; a backward of the first 70, of 64 x 128 instead 51.  With a column's rows over all 32
 // lanes (nine exchanges a token) these were 43 and 636.
 #include "linear.cuh"
 #include "tc_util.cuh"
@@ -36,7 +36,7 @@ template <int DA, int DC, bool PHASE1>
 constexpr int smem_floats = 2 * TT * ((PHASE1 ? 1 : 2) * DA + DC);
 
 template <int DA, int DC, bool PHASE1>
-__device__ __forceinline__ void token_run(const LinProblem &p, const LinRun &r, float *smem) {
+__device__ __forceinline__ void token_run(const LinProblem &p, const LinRun &r, unsigned block, float *smem) {
   constexpr int R = DA / 32, NT = DC * 8 / NC, HC = NC / 2;
   float(*tb)[TT][DA] = reinterpret_cast<float(*)[TT][DA]>(smem);
   float(*tcol)[TT][DC] = reinterpret_cast<float(*)[TT][DC]>(smem + 2 * TT * DA);
@@ -44,9 +44,8 @@ __device__ __forceinline__ void token_run(const LinProblem &p, const LinRun &r, 
   tc::griddep_wait();
   tc::griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31;
-  const unsigned blocks = gridDim.x / p.nrun, block = blockIdx.x % blocks;   // of this run's
   if (!PHASE1 && p.zero_rest && !r.y_f32)
-    lin_zero_rest(p, r.y, static_cast<size_t>(p.H) * DC * 4, lin_cu(p, 0), lin_cu(p, p.N), block, blocks);
+    lin_zero_rest(p, r.y, static_cast<size_t>(p.H) * DC * 4, lin_cu(p, 0), lin_cu(p, p.N), block, gridDim.x / p.nrun);
   if (tid >= NT) return;   // a narrow run beside wide ones
   const LinItem it = lin_item(p, block);
   const int h = it.h;
@@ -227,8 +226,8 @@ __device__ __forceinline__ void token_run(const LinProblem &p, const LinRun &r, 
   }
 }
 
-// All runs of a phase in one launch, one run's blocks after another's.  A forward has one run, (DA, DC); a backward
-// dq's, dk's and dv's, the last (DA, DC) and, if MIXED, the others (DC, DA).
+// All runs of a phase in one launch.  A forward has one run, (DA, DC); a backward dq's, dk's and dv's, the last (DA, DC)
+// and, if MIXED, the others (DC, DA).
 template <int DA, int DC, bool MIXED>
 constexpr int kBlock = (MIXED && DA > DC ? DA : DC) * 8 / NC;
 
@@ -236,9 +235,10 @@ template <int DA, int DC, bool PHASE1, bool MIXED>
 __global__ void __launch_bounds__(kBlock<DA, DC, MIXED>) linear_token_kernel(const __grid_constant__ LinProblem p) {
   constexpr int own = smem_floats<DA, DC, PHASE1>, other = MIXED ? smem_floats<DC, DA, PHASE1> : 0;
   __shared__ __align__(16) float smem[own > other ? own : other];
-  const LinRun &r = lin_run(p);
-  if (MIXED && r.dc != DC) token_run<DC, DA, PHASE1>(p, r, smem);
-  else token_run<DA, DC, PHASE1>(p, r, smem);
+  unsigned block;
+  const LinRun &r = lin_run<!MIXED>(p, block);
+  if (MIXED && r.dc != DC) token_run<DC, DA, PHASE1>(p, r, block, smem);
+  else token_run<DA, DC, PHASE1>(p, r, block, smem);
 }
 
 template <int DA, int DC, bool PHASE1, bool MIXED>
