@@ -15,7 +15,7 @@
 // before the first is used.  Whole rows (512 bytes per warp) where the batch
 // fills the device by itself; 32-column slices (128-byte row pieces) otherwise,
 // which puts four times the SMs on a small batch (3 rows of 8 heads of 128 x 128 in a
-// graph: 1.95 us in slices, 2.9 whole; 16 rows: 3.3 and 3.2; 36: 5.0 and 4.9).  256 rows
+// graph: 2.05 us in slices, 2.9 whole; 16 rows: 3.3 and 3.2; 36: 5.0 and 4.9).  256 rows
 // of 16 heads: 85.3 us, 6.27 TB/s; 3 rows of 8 heads called one by one: 11.8 us, the
 // host's part of a call.
 #include "linear.cuh"

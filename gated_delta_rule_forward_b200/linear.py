@@ -124,6 +124,13 @@ def linear_forward(q, k, v, *, log_decay, initial_state=None, output_final_state
     outside the pool reads zeros and writes nothing.  final_state may be
     initial_state; otherwise ``out`` and final_state overlap no input.  Returns
     (o [B,T,H,dv], final_state or None).
+
+    bf16: products on the tensor cores with fp32 sums, fp32 states; the attention
+    products and the state as a product's operand are rounded to bf16 once each, besides o
+    (2.4e-3 relative RMS in all).  o's last bits may depend on whether a final state
+    is wanted.  A NaN or an infinity in q, k or v reaches, besides the tokens after
+    its own, at most the other tokens of its block of 64 in its own sequence (fp32:
+    only those after it).
     """
     a, dims = _shape(q, k, v, log_decay, cu_seqlens)
     dt, B, T, Hk, H, dk, dv, N = dims
@@ -169,7 +176,7 @@ def linear_backward(q, k, v, d_o, *, log_decay, initial_state=None, d_final_stat
     [B,T,Hk,dk] (summed over the value heads that share a key head), v
     [B,T,H,dv] in the I/O type, and initial_state fp32 [N,H,dk,dv].  Rows behind
     the last packed sequence get zeros.  The decays are constants: they have no
-    gradient."""
+    gradient.  Rounding and non-finite values as in linear_forward."""
     a, dims = _shape(q, k, v, log_decay, cu_seqlens)
     dt, B, T, Hk, H, dk, dv, N = dims
     dev, f32 = q.device, torch.float32
@@ -203,7 +210,8 @@ def linear_decode_step(q, k, v, state, *, log_decay, state_slots=None, scale=1.0
     bf16 or fp32); state fp32 [pages,H,dk,dv], updated in place in page
     state_slots[n] (int32 [N], device; None: page n).  A row whose slot lies
     outside the pool is padding: its o is zeros and it touches no state.  The
-    slots inside the pool must differ from one another.  Returns o [N,H,dv]."""
+    slots inside the pool must differ from one another.  Computed in fp32, lambda in two
+    parts, so that thousands of steps stay within their roundings.  Returns o [N,H,dv]."""
     if q is None or v is None or state is None or q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
         raise ValueError("q must be [N,Hk,dk], v [N,H,dv] and state [pages,H,dk,dv]")
     N, Hk, dk = q.shape

@@ -310,8 +310,8 @@ gdr_status_t gdr_backward(int variant, int dtype, int B, int T, int H, int dk, i
  *    [0, pages) reads zeros and writes nothing.  The slots inside the pool must
  *    differ from one another.
  * A NaN or an infinity in q, k or v reaches, besides the tokens after its own,
- * at most the other tokens of its block of 64 (bf16; the fp32 kernels keep the
- * token order).
+ * at most the other tokens of its block of 64 in its own sequence (bf16; the fp32
+ * kernels keep the token order).
  */
 typedef struct {
     const void *q;               /* [B,T,Hk,dk] I/O dtype */
@@ -354,8 +354,12 @@ size_t gdr_linear_workspace_size(int dtype, int B, int T, int Hk, int H, int dk,
 /*
  * Whole-sequence forward.  Shapes: B, T, Hk, H, N >= 0; dk, dv in {64, 128};
  * bf16 or fp32.  bf16 products run on the tensor cores with fp32 accumulation;
- * the state is carried in fp32 and its update keeps fp32 accuracy; fp32 inputs
- * are computed in fp32.  An empty sequence copies its initial state to its
+ * the state is carried in fp32 and its update keeps fp32 accuracy (16 bits where it
+ * is not kept in final_state, so that o's last bits may depend on that).  On their way to
+ * o (and to the backward's gradients) the attention products with their decays, and the state as
+ * a product's operand, are rounded to bf16 once each, on disjoint parts of the sum:
+ * with o's own rounding 2.4e-3 relative RMS, where one rounding gives 1.7e-3.
+ * fp32 inputs are computed in fp32.  An empty sequence copies its initial state to its
  * final state.  The workspace (16-byte aligned, overwritten, not shared with a
  * call or graph that may run at the same time) may be NULL where
  * gdr_linear_workspace_size() is 0.
@@ -383,8 +387,9 @@ gdr_status_t gdr_linear_backward(int dtype, int B, int T, int Hk, int H, int dk,
  * state [pages,H,dk,dv] fp32, updated in place in page state_slots[n] (device,
  * int32), or in page n when state_slots is NULL.  A row whose slot lies outside
  * [0, pages) is padding: its o is zeros and it touches no state.  The slots
- * inside the pool must differ from one another.  One kernel launch, no
- * workspace.
+ * inside the pool must differ from one another.  Computed in fp32; lambda is taken in
+ * two parts, so that its rounding does not add up over a state's steps.  One
+ * kernel launch, no workspace.
  */
 gdr_status_t gdr_linear_decode_step(int dtype, int N, int Hk, int H, int dk, int dv, const void *q, const void *k,
                                     const void *v, const float *log_decay, float *state, int pages,
