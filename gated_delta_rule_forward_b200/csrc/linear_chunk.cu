@@ -35,7 +35,7 @@
 // Only S -> operand -> O1 is a chain from chunk to chunk.
 //
 // Measured on a B200 (bf16, d = 128): 65536 tokens of 16 heads, both phases, 306 us in thirty
-// calls after a rest and 363 us after seconds of them, when the power limit holds the clock at
+// calls after a rest and 363 to 373 us after seconds of them, when the power limit holds the clock at
 // 1.30 GHz; 8 sequences of 2048 tokens, 8 heads, 59 us forward and 112 us backward (1.73 GHz; 53 and 108 after a rest).
 // With 192 runs of 32 chunks the tensor pipe is active 43% of the time and 54% of the issue
 // slots are taken (1.73 GHz); a chunk takes about 2500 cycles, and value widths of 64 hardly
@@ -64,7 +64,8 @@ constexpr int C = 64;
 // warps 0-7 state, 8-15 output, 16-23 prep, then one for the copies and one for each of
 // the three kinds of products
 constexpr int NSTATE = 8, NOUT = 8, NPREP = 8;
-constexpr int W_OUT = NSTATE, W_PREP = W_OUT + NOUT, W_COPY = W_PREP + NPREP, W_MMA_P = W_COPY + 1, W_MMA_DS = W_COPY + 2;   // the last one: O
+constexpr int W_OUT = NSTATE, W_PREP = W_OUT + NOUT, W_COPY = W_PREP + NPREP, W_MMA_P = W_COPY + 1,
+              W_MMA_DS = W_COPY + 2;   // and the last warp: O
 constexpr int NTHREADS = 32 * (W_COPY + 4);
 // registers a thread: 72 at launch, moved to the threads that hold the state
 constexpr int R_STATE = 112, R_OUT = 64, R_PREP = 56, R_CTL = 40;

@@ -12,8 +12,8 @@
 //
 // Bound by the FMA pipe: 3 d^2 multiplications and additions a token are 200 ns of an
 // SM at d = 128; it takes 380 (the pipe 57% active).  Two sequences of 500 tokens, 4
-// heads: 33 us in a graph; 74 of 300, 8 heads: 460 us; a backward of the first 70, of 64 x 128 instead 51.  With a column's rows over all 32
-// lanes (nine exchanges a token) these were 43 and 636.
+// heads: 33 us in a graph, their backward 70; 74 of 300, 8 heads: 460 us.  With a column's rows
+// over all 32 lanes (nine exchanges a token) the forwards were 43 and 636.
 #include "linear.cuh"
 #include "tc_util.cuh"
 
